@@ -250,6 +250,122 @@ lsa_status lsa_sparse_attn_partial(const lsa_batch* batch, const void* q, int H,
 lsa_status lsa_merge_partials(const float* o_parts, const float* lse_parts, int n_parts, int T, int H, int Dv,
                               void* o, float* lse, void* stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ * A rotary embedding: pair i of the rot_dim rotated dimensions turns by position * inv_freq[i], and the
+ * rotated values are multiplied by mscale:
+ *   (u, w) -> mscale * (u cos a - w sin a, w cos a + u sin a),  a = position * inv_freq[i].
+ * The pairs are (i, i + rot_dim / 2) in the half layout, (2 i, 2 i + 1) in the interleaved one.  The struct
+ * is a host value: lsa_rope_init fills it once, every call that takes it reads it on the host during the
+ * call.  Angles are formed in 64 bits and reduced to one turn before the sine and cosine (32 bits), so far
+ * positions lose nothing; any int32 position is allowed, negative ones turn backwards. */
+#define LSA_ROPE_MAX_DIM 256
+#define LSA_ROPE_PLAIN  0 /* inv_freq[i] = theta^(-2 i / rot_dim) */
+#define LSA_ROPE_LINEAR 1 /* every frequency divided by factor */
+#define LSA_ROPE_NTK    2 /* theta multiplied by factor^(rot_dim / (rot_dim - 2)) */
+#define LSA_ROPE_YARN   3 /* frequencies that turn fewer than beta_slow times in orig_len positions divided by
+                           * factor, those above beta_fast kept, a linear ramp over the pairs between */
+typedef struct {
+    int32_t rot_dim;                       /* even, 2 .. LSA_ROPE_MAX_DIM */
+    int32_t interleaved;                   /* 0: half layout, 1: interleaved */
+    float   mscale;
+    int32_t reserved;
+    double  inv_freq[LSA_ROPE_MAX_DIM / 2];
+} lsa_rope;
+
+/* Fills *r (host memory).  scaling: LSA_ROPE_*; factor is read for all but LSA_ROPE_PLAIN (> 0), orig_len
+ * (>= 1), beta_fast and beta_slow (> 0) for LSA_ROPE_YARN.  theta > 1; mscale finite; LSA_ROPE_NTK needs
+ * rot_dim > 2. */
+lsa_status lsa_rope_init(lsa_rope* r, int rot_dim, int interleaved, double theta, int scaling, double factor,
+                         int64_t orig_len, double beta_fast, double beta_slow, double mscale);
+
+/* y[t,h,:] = x[t,h,:] with dimensions rope_off .. rope_off + rot_dim - 1 rotated by pos[t] (device [T]
+ * int32), the other of the D dimensions copied.  x and y: row (t, h) starts at t * tok_stride + h *
+ * head_stride elements (BF16, or FP32 with dtype LSA_FP32), dimensions contiguous, any alignment of whole
+ * elements (16-byte aligned rows are fastest).  y == x with equal strides rotates in place; x and y must
+ * not overlap otherwise.  backward != 0 rotates by the negative angle (times mscale): the gradient of x
+ * from the gradient of y.  Rounded once, from 32 bits.  T * H < 2^31, H <= 65,535, D <= 8192. */
+lsa_status lsa_rope_apply(const lsa_rope* r, int T, int H, int D, int rope_off, const int32_t* pos, int dtype,
+                          const void* x, int64_t x_tok_stride, int64_t x_head_stride,
+                          void* y, int64_t y_tok_stride, int64_t y_head_stride, int backward, void* stream);
+
+/* ---------------------------------------------------------------- paged caches
+ * With a page table, a cache is a pool of pages instead of one run of rows per sequence: position p of
+ * sequence b is row p % page_size of page table[b * ld + p / page_size], page i starting at
+ * data + i * seq_stride (scale + i * scale_seq_stride) -- the lsa_cache's "sequences" are the pages.  Calls
+ * that take an lsa_pages accept NULL for a cache without pages.  Entries past a sequence's last position are
+ * never read; an entry that is read and lies outside 0 .. n_pages - 1 is bad device data, and its rows are
+ * skipped (lsa_cache_append) or read as masked (attention). */
+typedef struct {
+    const int32_t* table;          /* device [B][ld] */
+    int64_t        ld;             /* entries between sequences, >= pages_per_seq */
+    int32_t        pages_per_seq;  /* entries of a sequence; pages_per_seq * page_size >= L_alloc */
+    int32_t        page_size;      /* rows per page: a multiple of 8 */
+    int32_t        n_pages;        /* pages in the pool */
+    int32_t        reserved;
+} lsa_pages;
+
+/* ---------------------------------------------------------------- cache append
+ * Stores one new row per query token in a cache: the row of token t goes to position q_pos[t] of sequence
+ * q_seq[t] (through `pages` when not NULL).  From x[t] (BF16, row t at x + t * ld_x, dim = cache->dim
+ * elements; 16-byte aligned rows):
+ *   1. the first norm_dim elements are normalised: LSA_NORM_RMS  h = x * rsqrt(mean(x^2) + eps) * gamma,
+ *      LSA_NORM_LAYER  h = (x - mean) * rsqrt(var + eps) * gamma + beta (gamma, beta: device FP32
+ *      [norm_dim], NULL = ones / zeros); LSA_NORM_NONE leaves them;
+ *   2. with `rope`, elements rope_off .. rope_off + rot_dim - 1 are rotated by q_pos[t];
+ *   3. the row is stored as BF16, or as e4m3 codes with scale = max|row| / 448 (1 for a row of zeros),
+ *      code = row * (448 / max|row|) rounded to nearest even.
+ * All in 32 bits, rounded once.  A latent row is [norm_dim = 512 normalised | 64 rotated]; an indexer key is
+ * layer-normalised whole and rotated in part.  A token with q_pos[t] < 0 is padding: nothing is stored.
+ * A row with a NaN or an infinity is reported (LSA_ERR_DEVICE_DATA) and stored as it is in a BF16 cache, as
+ * NaN codes with scale 1 in an FP8 cache; a position outside the sequence, or a bad page, is reported and
+ * nothing is stored.  Rows not named are left as they were.  A (sequence, position) may be named once per
+ * call.  cache->dim a multiple of 8 (16 for FP8), at most 1024; norm_dim a multiple of 8; the batch's q_group
+ * plays no part. */
+#define LSA_NORM_NONE  0
+#define LSA_NORM_RMS   1
+#define LSA_NORM_LAYER 2
+lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x, int norm, int norm_dim,
+                            const float* gamma, const float* beta, float eps, const lsa_rope* rope, int rope_off,
+                            const lsa_cache* cache, const lsa_pages* pages, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------- latent attention, absorbed form
+ * lsa_sparse_attn over every visible row: token t attends to rows 0 .. q_pos[t] of its sequence,
+ *   z_s = sm_scale * q[t,h,:] . K_s,  o[t,h,:] = sum_s softmax(z)_s V_s,  lse[t,h] = log sum_s exp(z_s),
+ * K_s = the 576 elements of row s, V_s = its first 512 (MLA absorbed layout), cache BF16 or FP8, paged or
+ * not: single tokens, verify tokens and prompt chunks behind a cached context.  The tokens of a group
+ * (q_group) belong to one sequence, that of the group's first token, and read its rows together.  A token
+ * with q_pos[t] < 0 is padding: o = 0, lse = -inf.  A position or a sequence outside the batch is reported
+ * and its token treated as padding.  Cached values at rows 0 .. the group's largest q_pos must be finite;
+ * what lies behind them may be anything.
+ *   q [T][H][576] BF16; o [T][H][512] of out_dtype (LSA_BF16, or LSA_FP32 for results that are merged later
+ *   with lsa_merge_partials); lse [T][H] float or NULL.  1 <= H <= 1024, q_group * H < 2^31 / 1024.
+ *   The work is cut evenly over the GPU by rows read, so ragged lengths need no split count; partial
+ *   results live in ws: lsa_latent_attn_workspace_size bytes, 256-byte aligned, not shared by calls that may
+ *   overlap. */
+lsa_status lsa_latent_attn(const lsa_batch* batch, const void* q, int H, const lsa_cache* kv,
+                           const lsa_pages* pages, float sm_scale, void* o, int out_dtype, float* lse,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+size_t lsa_latent_attn_workspace_size(int T, int q_group, int H);
+
+/* ---------------------------------------------------------------- latent attention, expanded form
+ * Attention of packed prompts or chunks with per-head keys and values expanded from the latent rows:
+ *   z = sm_scale * (q[t,h,0:128] . k_nope[s,h,:] + q[t,h,128:192] . k_rope[s,:]),
+ *   o[t,h,:] = sum_s softmax(z)_s v[s,h,:],  lse[t,h] = log sum_s exp(z_s).
+ * Sequence b owns query rows q_start[b] .. q_start[b+1] - 1 and key rows k_start[b] .. k_start[b+1] - 1
+ * (device int32 [B + 1], ascending, within 0 .. T and 0 .. S).  causal != 0: its last query sees its last
+ * key, query i (of nq) sees keys 0 .. i + nk - nq; a query that sees no key gets o = 0, lse = -inf.
+ * Query rows of no sequence are left as they were.  max_q: at least the longest nq (a sequence's queries
+ * beyond it are reported and not computed).  Strides in elements, rows 16-byte aligned:
+ *   q [T][H][192], k_nope [S][H][128], v [S][H][128], k_rope [S][64], all BF16 -- k_nope and v may be the
+ *   halves of one [S][H][256] projection; o [T][H][128] contiguous, of out_dtype (LSA_BF16 or LSA_FP32);
+ *   lse [T][H] float or NULL.  Keys and values of a sequence must be finite. */
+lsa_status lsa_latent_attn_expanded(int B, int T, int S, int H, int max_q, const int32_t* q_start,
+                                    const int32_t* k_start, const void* q, int64_t q_tok_stride,
+                                    int64_t q_head_stride, const void* k_nope, int64_t k_tok_stride,
+                                    int64_t k_head_stride, const void* k_rope, int64_t r_tok_stride, const void* v,
+                                    int64_t v_tok_stride, int64_t v_head_stride, float sm_scale, int causal, void* o,
+                                    int out_dtype, float* lse, int32_t* dev_status, void* stream);
+
 /* ---------------------------------------------------------------- KVP: one context over several ranks
  * [explainer] "③ KVP 解码切分示意" and [release] "推理" (decode nodes): the KV cache of a long
  * sequence is split over devices, each computes partial results over its shard, and the partial

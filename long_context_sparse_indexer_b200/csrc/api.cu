@@ -122,6 +122,23 @@ size_t attn_ws(int T, int H, int Dv, int n_split) {
 // default), set by lsa_set_wait_limit_ns.
 std::atomic<uint64_t> g_wait_limit_ns{0};
 
+// Checks of a page table and the cache whose pages it names (NULL: none).
+lsa_status check_pages(const lsa_pages* pg, const lsa_batch* batch) {
+    if (!pg) return LSA_OK;
+    if (pg->page_size < 1 || pg->pages_per_seq < 1 || pg->n_pages < 1 || pg->ld < pg->pages_per_seq) return LSA_ERR_INVALID_ARG;
+    if ((int64_t)pg->pages_per_seq * pg->page_size < batch->L_alloc) return LSA_ERR_INVALID_ARG;
+    if (!pg->table && batch->T > 0) return LSA_ERR_INVALID_ARG;
+    if (pg->page_size % 8) return LSA_ERR_UNSUPPORTED;
+    return LSA_OK;
+}
+
+// An lsa_rope as lsa_rope_init leaves it, rotating dimensions inside a row of `dim`.
+lsa_status check_rope(const lsa_rope* r, int off, int dim) {
+    if (!r || r->rot_dim < 2 || r->rot_dim > LSA_ROPE_MAX_DIM || r->rot_dim % 2) return LSA_ERR_INVALID_ARG;
+    if (off < 0 || (int64_t)off + r->rot_dim > dim) return LSA_ERR_INVALID_ARG;
+    return LSA_OK;
+}
+
 }  // namespace
 
 uint64_t lsa::wait_limit_ns() {
@@ -323,6 +340,129 @@ lsa_status lsa_topk(const lsa_batch* batch, const float* scores, int64_t ld_scor
                     void* stream) {
     return topk_impl(batch, scores, ld_scores, n_cols, cand_blocks, n_cand, block_size, k, n_sink, window, flags,
                      idx, ld_idx, count, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+lsa_status lsa_rope_init(lsa_rope* r, int rot_dim, int interleaved, double theta, int scaling, double factor,
+                         int64_t orig_len, double beta_fast, double beta_slow, double mscale) {
+    return rope_init(r, rot_dim, interleaved, theta, scaling, factor, orig_len, beta_fast, beta_slow, mscale);
+}
+
+lsa_status lsa_rope_apply(const lsa_rope* r, int T, int H, int D, int rope_off, const int32_t* pos, int dtype,
+                          const void* x, int64_t x_tok_stride, int64_t x_head_stride, void* y, int64_t y_tok_stride,
+                          int64_t y_head_stride, int backward, void* stream) {
+    lsa_status s = check_rope(r, rope_off, D);
+    if (s != LSA_OK) return s;
+    if (T < 0 || H < 0 || (int64_t)T * H > 0x7fffffff) return LSA_ERR_INVALID_ARG;
+    if (dtype != LSA_BF16 && dtype != LSA_FP32) return LSA_ERR_UNSUPPORTED;
+    if (D > 8192 || H > kMaxTokens) return LSA_ERR_UNSUPPORTED;
+    if (T == 0 || H == 0) return LSA_OK;
+    if (!pos || !x || !y) return LSA_ERR_INVALID_ARG;
+    const uintptr_t em = (uintptr_t)elem_bytes(dtype) - 1;
+    if (((uintptr_t)x & em) || ((uintptr_t)y & em) || ((uintptr_t)pos & 3)) return LSA_ERR_INVALID_ARG;
+    if (x == y && (x_tok_stride != y_tok_stride || x_head_stride != y_head_stride)) return LSA_ERR_INVALID_ARG;
+    // Rows written twice (a broadcast output) would race.
+    if ((T > 1 && y_tok_stride == 0) || (H > 1 && y_head_stride == 0)) return LSA_ERR_INVALID_ARG;
+    return cuda_status(launch_rope(r, T, H, D, rope_off, pos, dtype == LSA_BF16, x, x_tok_stride, x_head_stride, y,
+                                   y_tok_stride, y_head_stride, backward != 0, static_cast<cudaStream_t>(stream)));
+}
+
+lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x, int norm, int norm_dim,
+                            const float* gamma, const float* beta, float eps, const lsa_rope* rope, int rope_off,
+                            const lsa_cache* cache, const lsa_pages* pages, int32_t* dev_status, void* stream) {
+    lsa_status s = check_batch(batch);
+    if (s != LSA_OK) return s;
+    if ((s = check_cache(cache, 0)) != LSA_OK) return s;
+    if ((s = check_pages(pages, batch)) != LSA_OK) return s;
+    if (cache->dim > 1024) return LSA_ERR_UNSUPPORTED;
+    if (norm < LSA_NORM_NONE || norm > LSA_NORM_LAYER) return LSA_ERR_UNSUPPORTED;
+    if (norm != LSA_NORM_NONE) {
+        if (norm_dim < 8 || norm_dim > cache->dim || !(eps >= 0.f) || !std::isfinite(eps)) return LSA_ERR_INVALID_ARG;
+        if (norm_dim % 8) return LSA_ERR_UNSUPPORTED;
+        if (norm == LSA_NORM_RMS && beta) return LSA_ERR_INVALID_ARG;
+        if (((uintptr_t)gamma & 3) || ((uintptr_t)beta & 3)) return LSA_ERR_INVALID_ARG;
+    }
+    if (rope && (s = check_rope(rope, rope_off, cache->dim)) != LSA_OK) return s;
+    if (ld_x < cache->dim || ld_x % 8) return LSA_ERR_INVALID_ARG;
+    // Sequences (pages) that share their rows would be written over one another.
+    if ((pages ? pages->n_pages : batch->B) > 1 &&
+        (cache->seq_stride == 0 || (cache->dtype == LSA_FP8_E4M3 && cache->scale_seq_stride == 0)))
+        return LSA_ERR_INVALID_ARG;
+    if (batch->T == 0) return LSA_OK;
+    if (!x || !aligned16(x)) return LSA_ERR_INVALID_ARG;
+    AppendArgs a{};
+    a.seq_len = batch->seq_len; a.q_seq = batch->q_seq; a.q_pos = batch->q_pos;
+    a.B = batch->B; a.T = batch->T; a.L_alloc = batch->L_alloc;
+    a.x = static_cast<const uint16_t*>(x); a.ld_x = ld_x;
+    a.norm = norm; a.norm_dim = norm_dim; a.gamma = gamma; a.beta = norm == LSA_NORM_LAYER ? beta : nullptr; a.eps = eps;
+    a.rope_off = rope_off; a.dim = cache->dim;
+    const int eb = elem_bytes(cache->dtype);
+    a.data = static_cast<uint8_t*>(const_cast<void*>(cache->data));
+    a.scale = cache->dtype == LSA_FP8_E4M3 ? const_cast<float*>(cache->scale) : nullptr;
+    a.seq_b = cache->seq_stride * eb; a.tok_b = cache->tok_stride * eb; a.scale_seq = cache->scale_seq_stride;
+    if (pages) { a.table = pages->table; a.table_ld = pages->ld; a.page_size = pages->page_size; a.n_pages = pages->n_pages; }
+    a.status = dev_status;
+    return cuda_status(launch_append(a, rope, static_cast<cudaStream_t>(stream)));
+}
+
+size_t lsa_latent_attn_workspace_size(int T, int q_group, int H) {
+    if (T < 1 || q_group < 1 || H < 1) return 0;
+    return latent_attn_ws(T, q_group, H);
+}
+
+lsa_status lsa_latent_attn(const lsa_batch* batch, const void* q, int H, const lsa_cache* kv, const lsa_pages* pages,
+                           float sm_scale, void* o, int out_dtype, float* lse, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream) {
+    lsa_status s = check_batch(batch);
+    if (s != LSA_OK) return s;
+    if ((s = check_cache(kv, 576)) != LSA_OK) return s;
+    if ((s = check_pages(pages, batch)) != LSA_OK) return s;
+    if (H < 1 || !(sm_scale > 0.f) || !std::isfinite(sm_scale)) return LSA_ERR_INVALID_ARG;
+    if (H > 1024 || (int64_t)batch->q_group * H >= 0x7fffffff / 1024) return LSA_ERR_UNSUPPORTED;
+    if (out_dtype != LSA_BF16 && out_dtype != LSA_FP32) return LSA_ERR_UNSUPPORTED;
+    if (batch->T == 0) return LSA_OK;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3)) return LSA_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < latent_attn_ws(batch->T, batch->q_group, H) || ((uintptr_t)ws % kAlign)) return LSA_ERR_WORKSPACE;
+    LatentArgs a{};
+    a.seq_len = batch->seq_len; a.q_seq = batch->q_seq; a.q_pos = batch->q_pos;
+    a.B = batch->B; a.T = batch->T; a.q_group = batch->q_group; a.L_alloc = batch->L_alloc;
+    a.q = static_cast<const uint16_t*>(q); a.H = H;
+    const int eb = elem_bytes(kv->dtype);
+    a.kv = static_cast<const uint8_t*>(kv->data);
+    a.kv_scale = kv->dtype == LSA_FP8_E4M3 ? kv->scale : nullptr;
+    a.seq_b = kv->seq_stride * eb; a.tok_b = kv->tok_stride * eb; a.scale_seq = kv->scale_seq_stride;
+    a.page_size = batch->L_alloc; a.n_pages = batch->B;
+    if (pages) { a.table = pages->table; a.table_ld = pages->ld; a.page_size = pages->page_size; a.n_pages = pages->n_pages; }
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.o = o; a.o_f32 = out_dtype == LSA_FP32; a.lse = lse; a.ws = ws; a.status = dev_status;
+    return cuda_status(launch_latent_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+lsa_status lsa_latent_attn_expanded(int B, int T, int S, int H, int max_q, const int32_t* q_start,
+                                    const int32_t* k_start, const void* q, int64_t q_tok_stride,
+                                    int64_t q_head_stride, const void* k_nope, int64_t k_tok_stride,
+                                    int64_t k_head_stride, const void* k_rope, int64_t r_tok_stride, const void* v,
+                                    int64_t v_tok_stride, int64_t v_head_stride, float sm_scale, int causal, void* o,
+                                    int out_dtype, float* lse, int32_t* dev_status, void* stream) {
+    if (B < 0 || T < 0 || S < 0 || H < 1 || max_q < 0) return LSA_ERR_INVALID_ARG;
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return LSA_ERR_INVALID_ARG;
+    if (out_dtype != LSA_BF16 && out_dtype != LSA_FP32) return LSA_ERR_UNSUPPORTED;
+    if (B > kMaxTokens || H > 1024) return LSA_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0 || max_q == 0) return LSA_OK;
+    if (!q_start || !k_start || !q || !o || ((uintptr_t)lse & 3)) return LSA_ERR_INVALID_ARG;
+    if (S > 0 && (!k_nope || !k_rope || !v)) return LSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v) || !aligned16(o)) return LSA_ERR_INVALID_ARG;
+    for (int64_t st : {q_tok_stride, q_head_stride, k_tok_stride, k_head_stride, r_tok_stride, v_tok_stride, v_head_stride})
+        if (st < 0 || st % 8) return LSA_ERR_INVALID_ARG;
+    ExpandedArgs a{};
+    a.B = B; a.T = T; a.S = S; a.H = H; a.max_q = max_q < T ? max_q : T;
+    a.q_start = q_start; a.k_start = k_start;
+    a.q = static_cast<const uint16_t*>(q); a.kn = static_cast<const uint16_t*>(k_nope);
+    a.kr = static_cast<const uint16_t*>(k_rope); a.v = static_cast<const uint16_t*>(v);
+    a.qt = q_tok_stride; a.qh = q_head_stride; a.kt = k_tok_stride; a.kh = k_head_stride; a.rt = r_tok_stride;
+    a.vt = v_tok_stride; a.vh = v_head_stride;
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f; a.causal = causal != 0;
+    a.o = o; a.o_f32 = out_dtype == LSA_FP32; a.lse = lse; a.status = dev_status;
+    return cuda_status(launch_latent_expanded(a, static_cast<cudaStream_t>(stream)));
 }
 
 lsa_status lsa_sparse_attn(const lsa_batch* batch, const void* q, int H, int Dqk, const lsa_cache* kv,

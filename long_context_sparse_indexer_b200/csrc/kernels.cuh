@@ -160,6 +160,81 @@ cudaError_t launch_kvp_local_index(int T, int B, const int32_t* q_seq, const int
                                    const int32_t* count, int32_t* local_idx, int64_t ld_local, int32_t* local_count,
                                    int32_t* status, cudaStream_t st);
 
+// Rotary positions (rope.cu).
+struct RopeTable;
+RopeTable rope_table(const lsa_rope* r);
+lsa_status rope_init(lsa_rope* r, int rot_dim, int interleaved, double theta, int scaling, double factor,
+                     int64_t orig_len, double beta_fast, double beta_slow, double mscale);
+cudaError_t launch_rope(const lsa_rope* r, int T, int H, int D, int off, const int32_t* pos, bool bf16, const void* x,
+                        int64_t xt, int64_t xh, void* y, int64_t yt, int64_t yh, bool backward, cudaStream_t st);
+
+// Cache append (append.cu).
+struct AppendArgs {
+    const int32_t* seq_len;
+    const int32_t* q_seq;
+    const int32_t* q_pos;
+    int B, T, L_alloc;
+    const uint16_t* x;           // bf16 bits, row t at x + t * ld_x
+    int64_t ld_x;
+    int norm, norm_dim;
+    const float* gamma;
+    const float* beta;
+    float eps;
+    int rope, rope_off;          // rope: set by the launcher
+    int dim;
+    uint8_t* data;               // cache base (bytes), strides in bytes; pages in place of sequences with a table
+    float* scale;                // FP8: per-row scale, else NULL
+    int64_t seq_b, tok_b, scale_seq;
+    const int32_t* table;        // page table or NULL
+    int64_t table_ld;
+    int page_size, n_pages;
+    int32_t* status;
+};
+cudaError_t launch_append(const AppendArgs& a, const lsa_rope* rope, cudaStream_t st);
+
+// Latent attention, absorbed form (latent_attn.cu).
+struct LatentArgs {
+    const int32_t* seq_len;
+    const int32_t* q_seq;
+    const int32_t* q_pos;
+    int B, T, q_group, L_alloc;
+    const uint16_t* q;           // [T][H][576] bf16
+    int H;
+    const uint8_t* kv;           // cache base (bytes), strides in bytes; pages in place of sequences with a table
+    const float* kv_scale;       // FP8: per-row scale, else NULL
+    int64_t seq_b, tok_b, scale_seq;
+    const int32_t* table;
+    int64_t table_ld;
+    int page_size, n_pages;      // without a table: L_alloc and B
+    float sm_scale_log2;         // sm_scale * log2(e)
+    void* o;                     // [T][H][512] bf16 or float
+    int o_f32;
+    float* lse;                  // [T][H] or NULL
+    void* ws;
+    int32_t* status;
+};
+size_t latent_attn_ws(int T, int q_group, int H);
+cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st);
+
+// Latent attention, expanded form (latent_expanded.cu).
+struct ExpandedArgs {
+    int B, T, S, H, max_q;
+    const int32_t* q_start;
+    const int32_t* k_start;
+    const uint16_t* q;           // strides in elements
+    const uint16_t* kn;
+    const uint16_t* kr;
+    const uint16_t* v;
+    int64_t qt, qh, kt, kh, rt, vt, vh;
+    float sm_scale_log2;
+    int causal;
+    void* o;                     // [T][H][128] bf16 or float
+    int o_f32;
+    float* lse;
+    int32_t* status;
+};
+cudaError_t launch_latent_expanded(const ExpandedArgs& a, cudaStream_t st);
+
 // Wait limit the tensor-core indexer and block-score kernels are launched with (api.cu).
 uint64_t wait_limit_ns();
 

@@ -53,6 +53,16 @@ class CLayer(ctypes.Structure):
     _fields_ = [("q", c_vp), ("kv", CCache), ("v", CCache), ("o", c_vp), ("lse", c_vp)]
 
 
+class CRope(ctypes.Structure):
+    _fields_ = [("rot_dim", c_i32), ("interleaved", c_i32), ("mscale", c_f32), ("reserved", c_i32),
+                ("inv_freq", ctypes.c_double * 128)]
+
+
+class CPages(ctypes.Structure):
+    _fields_ = [("table", c_vp), ("ld", c_i64), ("pages_per_seq", c_i32), ("page_size", c_i32), ("n_pages", c_i32),
+                ("reserved", c_i32)]
+
+
 class CDecodeParams(ctypes.Structure):
     _fields_ = [("batch", CBatch), ("q_idx", c_vp), ("w", c_vp), ("H_I", c_i32), ("k_idx", CCache),
                 ("k", c_i32), ("n_sink", c_i32), ("window", c_i32),
@@ -95,6 +105,19 @@ _lib.lsa_kvp_select_workspace_size.restype = c_size
 _lib.lsa_kvp_select.argtypes = [_P(CBatch), c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp,
                                 c_size, c_vp, c_vp]
 _lib.lsa_kvp_local_index.argtypes = [_P(CBatch), c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp]
+c_f64 = ctypes.c_double
+_lib.lsa_rope_init.argtypes = [_P(CRope), c_i32, c_i32, c_f64, c_i32, c_f64, c_i64, c_f64, c_f64, c_f64]
+_lib.lsa_rope_apply.argtypes = [_P(CRope), c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_i64, c_i64, c_vp, c_i64,
+                                c_i64, c_i32, c_vp]
+_lib.lsa_cache_append.argtypes = [_P(CBatch), c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_f32, _P(CRope), c_i32, _P(CCache),
+                                  _P(CPages), c_vp, c_vp]
+_lib.lsa_latent_attn.argtypes = [_P(CBatch), c_vp, c_i32, _P(CCache), _P(CPages), c_f32, c_vp, c_i32, c_vp, c_vp, c_size,
+                                 c_vp, c_vp]
+_lib.lsa_latent_attn_workspace_size.argtypes = [c_i32, c_i32, c_i32]
+_lib.lsa_latent_attn_workspace_size.restype = c_size
+_lib.lsa_latent_attn_expanded.argtypes = [c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_i64,
+                                          c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_f32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                          c_vp]
 
 
 class CCopy(ctypes.Structure):
@@ -113,7 +136,8 @@ _lib.lsa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.lsa_set_wait_limit_ns.restype = ctypes.c_uint64
 for _f in ("lsa_index_score", "lsa_index_score_q8", "lsa_block_keys", "lsa_block_score", "lsa_topk", "lsa_sparse_attn",
            "lsa_sparse_attn_noalloc", "lsa_decode_fused", "lsa_read_device_status", "lsa_sparse_attn_partial",
-           "lsa_merge_partials", "lsa_kvp_shard_batch", "lsa_kvp_candidates", "lsa_kvp_select", "lsa_kvp_local_index"):
+           "lsa_merge_partials", "lsa_kvp_shard_batch", "lsa_kvp_candidates", "lsa_kvp_select", "lsa_kvp_local_index",
+           "lsa_rope_init", "lsa_rope_apply", "lsa_cache_append", "lsa_latent_attn", "lsa_latent_attn_expanded"):
     getattr(_lib, _f).restype = c_i32
 
 EXPORTS = ("lsa_index_score", "lsa_index_score_q8", "lsa_block_keys", "lsa_block_score", "lsa_topk", "lsa_sparse_attn",
@@ -121,7 +145,8 @@ EXPORTS = ("lsa_index_score", "lsa_index_score_q8", "lsa_block_keys", "lsa_block
            "lsa_status_string", "lsa_version", "lsa_pipeline_create", "lsa_pipeline_step", "lsa_pipeline_join",
            "lsa_pipeline_destroy", "lsa_sparse_attn_partial", "lsa_merge_partials", "lsa_kvp_shard_batch",
            "lsa_kvp_candidates", "lsa_kvp_select_workspace_size", "lsa_kvp_select", "lsa_kvp_local_index",
-           "lsa_set_wait_limit_ns", "lsa_decode_index_capacity")
+           "lsa_set_wait_limit_ns", "lsa_decode_index_capacity", "lsa_rope_init", "lsa_rope_apply", "lsa_cache_append",
+           "lsa_latent_attn", "lsa_latent_attn_workspace_size", "lsa_latent_attn_expanded")
 
 
 def library() -> ctypes.CDLL:
@@ -344,6 +369,191 @@ def kvp_local_index(batch: Batch, shard_start: torch.Tensor, shard_len: torch.Te
     _check(_lib.lsa_kvp_local_index(ctypes.byref(cb), _ptr(shard_start), _ptr(shard_len), _ptr(idx),
                                     int(idx.stride(0)), _ptr(count), _ptr(local_idx), int(local_idx.stride(0)),
                                     _ptr(local_count), _ptr(dev_status), _stream(stream)), "lsa_kvp_local_index")
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor on the current CUDA device, where the call is launched."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensor on {t.device}: the call runs on the current device (cuda:{dev})")
+
+
+def _float_vec(t: Optional[torch.Tensor], n: int, name: str) -> None:
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n):
+        raise ValueError(f"{name}: a contiguous float32 tensor of {n} elements")
+
+
+def _int_vec(t: torch.Tensor, n: int, name: str) -> None:
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements")
+
+
+def _check_batch_vecs(b: Batch) -> None:
+    _int_vec(b.q_seq, b.q_seq.numel(), "q_seq")
+    _int_vec(b.q_pos, b.q_seq.numel(), "q_pos")
+    _int_vec(b.seq_len, b.seq_len.numel(), "seq_len")
+
+
+def _check_cache(c: Cache) -> None:
+    if c.data.dim() != 3 or c.data.stride(2) != 1:
+        raise ValueError("cache: [sequences or pages, rows, dim] with contiguous rows")
+    if c.dtype == FP8_E4M3 and (c.scale is None or c.scale.dtype != torch.float32 or c.scale.dim() != 2
+                                or c.scale.stride(1) != 1 or c.scale.shape != c.data.shape[:2]):
+        raise ValueError("cache scale: float32 [sequences or pages, rows] with contiguous rows")
+
+
+class Rope:
+    """A rotary embedding (lsa_rope): `rot_dim` dimensions in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when
+    interleaved, turning by position * theta^(-2i / rot_dim); scaling: "none", "linear", "ntk" or "yarn"
+    (lsa_rope_init).  Host data, made once and kept."""
+    SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, orig_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 mscale: float = 1.0):
+        if scaling not in self.SCALING:
+            raise ValueError(f"unknown rope scaling {scaling!r}")
+        self.c = CRope()
+        _check(_lib.lsa_rope_init(ctypes.byref(self.c), int(rot_dim), int(bool(interleaved)), float(theta),
+                                  self.SCALING[scaling], float(factor), int(orig_len), float(beta_fast),
+                                  float(beta_slow), float(mscale)), "lsa_rope_init")
+
+    @property
+    def inv_freq(self):
+        """The rot_dim / 2 angles per position."""
+        return list(self.c.inv_freq[:self.c.rot_dim // 2])
+
+
+@dataclass
+class PageTable:
+    """The pages of every sequence, [B, pages per sequence] int32 on the device: with it a Cache is a pool
+    [pages, page rows, dim], and position p of sequence b is row p % page rows of page table[b, p // page rows]."""
+    table: torch.Tensor
+
+    def c(self, cache: Cache) -> CPages:
+        t = self.table
+        if t.dim() != 2 or t.dtype != torch.int32 or t.stride(1) != 1:
+            raise ValueError("page table: int32 [sequences, pages per sequence] with contiguous rows")
+        return CPages(_ptr(t), int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1]), int(t.shape[1]),
+                      int(cache.data.shape[1]), int(cache.data.shape[0]), 0)
+
+
+def _pages(pages: Optional[PageTable], cache: Cache, batch: Batch):
+    """The C page table of a checked cache, or None; a cache without pages holds the batch's sequences."""
+    _check_cache(cache)
+    if pages is None:
+        if cache.data.shape[0] < batch.seq_len.numel() or cache.data.shape[1] < batch.L_alloc:
+            raise ValueError("cache: fewer sequences or rows than the batch")
+        return None
+    if pages.table.shape[0] < batch.seq_len.numel():
+        raise ValueError("page table: fewer sequences than the batch")
+    return ctypes.byref(pages.c(cache))
+
+
+def rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: Optional[torch.Tensor] = None, offset: int = 0,
+         backward: bool = False, stream=None) -> torch.Tensor:
+    """lsa_rope_apply: dimensions [offset, offset + rot_dim) of x [T, H, D] (bf16 or float32, any strides with
+    contiguous dimensions) rotated by pos [T] int32 into y, in place when y is None.  backward: the rotation by
+    the negative angle, which takes the gradient of y to that of x.  Returns y."""
+    y = x if y is None else y
+    if x.dim() != 3 or y.shape != x.shape or y.dtype != x.dtype or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("rope: x and y are [T, H, D] of one type, bf16 or float32")
+    if x.shape[2] > 1 and (x.stride(2) != 1 or y.stride(2) != 1):
+        raise ValueError("rope: the last dimension is contiguous")
+    T, H, D = (int(n) for n in x.shape)
+    _int_vec(pos, T, "pos")
+    _same_device(pos, x, y)
+    # A dimension of one element has no stride that matters (and may report zero for an expanded one).
+    st = lambda t, i: int(t.stride(i)) if t.shape[i] > 1 else D  # noqa: E731
+    _check(_lib.lsa_rope_apply(ctypes.byref(rope.c), T, H, D, int(offset), _ptr(pos),
+                               BF16 if x.dtype == torch.bfloat16 else FP32, _ptr(x), st(x, 0), st(x, 1), _ptr(y),
+                               st(y, 0), st(y, 1), int(bool(backward)), _stream(stream)), "lsa_rope_apply")
+    return y
+
+
+def cache_append(batch: Batch, x: torch.Tensor, cache: Cache, pages: Optional[PageTable] = None, norm: str = "none",
+                 norm_dim: int = 0, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, rope: Optional[Rope] = None, rope_offset: int = 0,
+                 dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """lsa_cache_append: the rows x [T, dim] (bf16), normalised ("none", "rms" or "layer" over the first norm_dim
+    elements, default all), rotated (rope, at rope_offset) and stored at each token's position of the cache."""
+    kinds = {"none": 0, "rms": 1, "layer": 2}
+    if norm not in kinds:
+        raise ValueError(f"unknown norm {norm!r}")
+    T, dim = int(batch.q_seq.numel()), int(cache.data.shape[2])
+    if x.dim() != 2 or x.shape[0] != T or x.shape[1] != dim or x.dtype != torch.bfloat16 or x.stride(1) != 1:
+        raise ValueError("cache_append: x is [T, dim] bf16 with contiguous rows")
+    norm_dim = int(norm_dim or dim)
+    _float_vec(gamma, norm_dim, "gamma")
+    _float_vec(beta, norm_dim, "beta")
+    _check_batch_vecs(batch)
+    cp = _pages(pages, cache, batch)
+    _same_device(x, cache.data, cache.scale, gamma, beta, dev_status, batch.q_pos, batch.q_seq, batch.seq_len,
+                 pages.table if pages else None)
+    cb, cc = batch.c(), cache.c()
+    _check(_lib.lsa_cache_append(ctypes.byref(cb), _ptr(x), int(x.stride(0)) if T > 1 else dim, kinds[norm], norm_dim,
+                                 _ptr(gamma), _ptr(beta), float(eps), ctypes.byref(rope.c) if rope else None,
+                                 int(rope_offset), ctypes.byref(cc), cp, _ptr(dev_status), _stream(stream)),
+           "lsa_cache_append")
+
+
+def latent_attn_workspace_size(T: int, q_group: int, H: int) -> int:
+    return int(_lib.lsa_latent_attn_workspace_size(T, q_group, H))
+
+
+def _out_dtype(o: torch.Tensor, shape) -> int:
+    if tuple(o.shape) != tuple(shape) or not o.is_contiguous() or o.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"o: contiguous bf16 or float32 {list(shape)}")
+    return BF16 if o.dtype == torch.bfloat16 else FP32
+
+
+def latent_attn(batch: Batch, q: torch.Tensor, cache: Cache, sm_scale: float, o: torch.Tensor,
+                lse: Optional[torch.Tensor] = None, pages: Optional[PageTable] = None, ws: Optional[torch.Tensor] = None,
+                dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """lsa_latent_attn: q [T, H, 576] bf16 over every cached row up to each token's position -> o [T, H, 512]
+    (bf16, or float32 for a later merge_partials), lse [T, H] float32.  ws: latent_attn_workspace_size bytes."""
+    T = int(batch.q_seq.numel())
+    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != 576 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("latent_attn: q is contiguous bf16 [T, H, 576]")
+    H = int(q.shape[1])
+    dt = _out_dtype(o, (T, H, 512))
+    _float_vec(lse, T * H, "lse")
+    _check_batch_vecs(batch)
+    cp = _pages(pages, cache, batch)
+    _same_device(q, o, lse, ws, dev_status, cache.data, cache.scale, batch.q_pos, batch.q_seq, batch.seq_len,
+                 pages.table if pages else None)
+    cb, cc = batch.c(), cache.c()
+    _check(_lib.lsa_latent_attn(ctypes.byref(cb), _ptr(q), H, ctypes.byref(cc), cp, float(sm_scale), _ptr(o), dt,
+                                _ptr(lse), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
+                                _ptr(dev_status), _stream(stream)), "lsa_latent_attn")
+
+
+def latent_attn_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                         q_start: torch.Tensor, k_start: torch.Tensor, max_q: int, sm_scale: float, o: torch.Tensor,
+                         lse: Optional[torch.Tensor] = None, causal: bool = True,
+                         dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """lsa_latent_attn_expanded: packed sequences, q [T, H, 192], k_nope and v [S, H, 128] and the shared k_rope
+    [S, 64] (bf16, contiguous last dimension) -> o [T, H, 128] (bf16 or float32), lse [T, H] float32.  q_start /
+    k_start [B + 1] int32: the sequences' rows; max_q: the longest sequence's query count."""
+    if (q.dim() != 3 or q.shape[2] != 192 or k_nope.dim() != 3 or k_nope.shape[1:] != (q.shape[1], 128)
+            or v.shape != k_nope.shape or k_rope.shape != (k_nope.shape[0], 64)):
+        raise ValueError("latent_attn_expanded: q [T, H, 192], k_nope and v [S, H, 128], k_rope [S, 64]")
+    if any(t.dtype != torch.bfloat16 or t.stride(-1) != 1 for t in (q, k_nope, k_rope, v)):
+        raise ValueError("latent_attn_expanded: bf16 inputs with a contiguous last dimension")
+    T, H, S = int(q.shape[0]), int(q.shape[1]), int(k_nope.shape[0])
+    dt = _out_dtype(o, (T, H, 128))
+    _float_vec(lse, T * H, "lse")
+    B = int(q_start.numel()) - 1
+    _int_vec(q_start, B + 1, "q_start")
+    _int_vec(k_start, B + 1, "k_start")
+    _same_device(q, k_nope, k_rope, v, q_start, k_start, o, lse, dev_status)
+    # A dimension of one element has no stride that matters.
+    st = lambda t, i: int(t.stride(i)) if t.shape[i] > 1 else 0  # noqa: E731
+    _check(_lib.lsa_latent_attn_expanded(B, T, S, H, int(max_q), _ptr(q_start), _ptr(k_start), _ptr(q), st(q, 0), st(q, 1),
+                                         _ptr(k_nope), st(k_nope, 0), st(k_nope, 1), _ptr(k_rope), st(k_rope, 0),
+                                         _ptr(v), st(v, 0), st(v, 1), float(sm_scale), int(bool(causal)), _ptr(o), dt,
+                                         _ptr(lse), _ptr(dev_status), _stream(stream)), "lsa_latent_attn_expanded")
 
 
 @dataclass
