@@ -453,6 +453,9 @@ lsa_status lsa_latent_attn_expanded(int B, int T, int S, int H, int max_q, const
     if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v) || !aligned16(o)) return LSA_ERR_INVALID_ARG;
     for (int64_t st : {q_tok_stride, q_head_stride, k_tok_stride, k_head_stride, r_tok_stride, v_tok_stride, v_head_stride})
         if (st < 0 || st % 8) return LSA_ERR_INVALID_ARG;
+    // Heads may share rows (stride 0), tokens may not.
+    if ((T > 1 && q_tok_stride == 0) || (S > 1 && (k_tok_stride == 0 || r_tok_stride == 0 || v_tok_stride == 0)))
+        return LSA_ERR_INVALID_ARG;
     ExpandedArgs a{};
     a.B = B; a.T = T; a.S = S; a.H = H; a.max_q = max_q < T ? max_q : T;
     a.q_start = q_start; a.k_start = k_start;

@@ -1,103 +1,401 @@
-// Latent attention in the expanded form: packed prompts with per-head keys and values, 64 shared rotary
-// dimensions.
+// Latent attention in the expanded form on the 5th-generation tensor cores: packed prompts with per-head keys
+// and values, 64 rotary dimensions shared by the heads.
 //
-//   z = sm_scale (q[0:128] . k_nope + q[128:192] . k_rope), o = softmax(z) v.
+//   z = sm_scale (q[0:128] . k_nope + q[128:192] . k_rope), o = softmax(z) v, one pass over the keys with a
+//   running reference maximum and sum.
 //
-// One pass with a running maximum and sum.  Block = (16 queries of a sequence, head): FP32 on CUDA cores,
-// tiles of 16 keys, each thread two of the 16 x 16 scores and one of the 128 value dimensions of all 16 queries.
+// Work split.  CTA = 256 queries of one (sequence, head) as two tiles of M = 128 rows, against 128 keys at a
+// time: each key tile is loaded once for both.  The two tiles take turns on the tensor pipe -- while one
+// tile's 128 x 128 scores are in the softmax, the other's products run (O0 += P0 V, S0', O1 += P1 V, S1', ...).
+// Per key tile and query tile the pipe needs 12 + 8 MMAs of 64 cycles (S: K = 192; P V: K = 128, N = 128), the
+// softmax 16,384 exponentials of 16 a cycle = 1,024 cycles: both pipes are close to full, the tensor one first.
+//
+// Memory.  TMEM (512 columns): S0, S1 (128 each; the softmax writes P as BF16 over the S it has read), O0, O1
+// (128 each).  Shared memory: Q (2 x 3 swizzled 64-dim atoms, 96 KB) and a ring of eight 16 KB units: a key
+// tile is five units, three K atoms (64 dims x 128 keys; two of k_nope, the rotary one) and two V units (64 keys
+// x 128 dims), each released as soon as its last product is issued.
+//
+// Warps: 0..3 softmax of query tile 0 (thread = row = TMEM lane), 4..7 of tile 1, 8 issues the MMAs, 9 the TMA
+// loads, 10 clears the rows of the last key tile that lie behind the sequence (0 x whatever they hold would
+// reach O).  All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
+#include <cstring>
 
 #include "kernels.cuh"
+#include "tc.cuh"
 
 namespace lsa {
 
 namespace {
 
-constexpr int kThreads = 128, kQ = 16, kRows = 16, kDn = 128, kDr = 64, kD = kDn + kDr, kDv = 128;
+constexpr int kThreads = 384;
+constexpr int kM = 128, kN = 128;                // query rows of a tile, keys of a tile
+constexpr int kDn = 128, kDr = 64, kD = kDn + kDr, kDv = 128;
+constexpr int kUnits = 8, kUnitBytes = 16384;    // ring
+constexpr int kPerTile = 5;                      // units of a key tile: K atoms 0..2, V keys 0..63, 64..127
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split within the launch's registers");
 
 struct Smem {
-    float q[kQ][kD + 1];
-    float k[kRows][kD + 1];
-    float v[kRows][kDv];
-    float p[kQ][kRows];
-    float m[kQ], l[kQ], alpha[kQ];
+    alignas(1024) uint8_t q[2][3][kM * 128];     // query tiles, 64-dim atoms
+    alignas(1024) uint8_t ring[kUnits][kUnitBytes];
+    uint64_t full[kUnits], empty[kUnits];
+    uint64_t q_full;
+    uint64_t v_last[2];                          // a partial last tile's V units: landed, not yet cleared behind the sequence
+    uint64_t mma_done;                           // committed once, after the last MMA (the issuer's drain)
+    uint64_t s_full[2], p_full[2][2], o_done[2]; // p_full[tile][keys 0..63 / 64..127]
+    uint32_t tmem_base;
+    int abort;
 };
 
-__global__ void __launch_bounds__(kThreads) latent_expanded_kernel(ExpandedArgs a) {
-    extern __shared__ uint8_t raw[];
-    Smem& s = *reinterpret_cast<Smem*>(raw);
-    const int i0 = blockIdx.x * kQ, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    const int qs = a.q_start[b], nq = a.q_start[b + 1] - qs, ks = a.k_start[b], nk = a.k_start[b + 1] - ks;
-    const bool ok = qs >= 0 && nq >= 0 && nq <= a.max_q && qs + (int64_t)nq <= a.T && ks >= 0 && nk >= 0 && ks + (int64_t)nk <= a.S;
-    if (!ok && i0 == 0 && h == 0 && tid == 0) report(a.status, LSA_ERR_DEVICE_DATA);
-    if (qs < 0 || nq < 0 || qs + (int64_t)nq > a.T || ks < 0 || nk < 0 || ks + (int64_t)nk > a.S) return;
-    const int n = min(kQ, min(nq, a.max_q) - i0);
-    if (n <= 0) return;
-    for (int i = tid; i < kQ * kD; i += kThreads) {
-        const int r = i / kD, d = i % kD;
-        s.q[r][d] = r < n ? bf16_bits_to_float(a.q[(qs + i0 + r) * a.qt + h * a.qh + d]) * a.sm_scale_log2 : 0.f;
-    }
-    if (tid < kQ) { s.m[tid] = kNegInf; s.l[tid] = 0.f; }
-    float acc[kQ];
-#pragma unroll
-    for (int r = 0; r < kQ; ++r) acc[r] = 0.f;
-    const int end = a.causal ? min(nk, i0 + n + nk - nq) : nk;
-    for (int k0 = 0; k0 < end; k0 += kRows) {
-        __syncthreads();
-        for (int i = tid; i < kRows * kD; i += kThreads) {
-            const int r = i / kD, d = i % kD;
-            const int64_t j = ks + k0 + r;
-            s.k[r][d] = k0 + r >= end ? 0.f
-                : bf16_bits_to_float(d < kDn ? a.kn[j * a.kt + h * a.kh + d] : a.kr[j * a.rt + d - kDn]);
-            if (d < kDv) s.v[r][d] = k0 + r >= end ? 0.f : bf16_bits_to_float(a.v[j * a.vt + h * a.vh + d]);
-        }
-        __syncthreads();
-        for (int i = tid; i < kQ * kRows; i += kThreads) {
-            const int r = i / kRows, j = i % kRows;
-            float z = 0.f;
-            for (int d = 0; d < kD; ++d) z = fmaf(s.q[r][d], s.k[j][d], z);
-            const bool seen = k0 + j < end && (!a.causal || k0 + j <= i0 + r + nk - nq);
-            s.p[r][j] = seen ? z : kNegInf;
-        }
-        __syncthreads();
-        if (tid < kQ) {
-            float m = s.m[tid];
-            for (int j = 0; j < kRows; ++j) m = fmaxf(m, s.p[tid][j]);
-            const float ref = m == kNegInf ? 0.f : m;
-            const float al = exp2f(s.m[tid] - ref);
-            float l = s.l[tid] * al;
-            for (int j = 0; j < kRows; ++j) {
-                s.p[tid][j] = exp2f(s.p[tid][j] - ref);
-                l += s.p[tid][j];
-            }
-            s.m[tid] = m; s.l[tid] = l; s.alpha[tid] = al;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kQ; ++r) {
-            float v = acc[r] * s.alpha[r];
-            for (int j = 0; j < kRows; ++j) v = fmaf(s.p[r][j], s.v[j][tid], v);
-            acc[r] = v;
+struct Plan {
+    int q0, rows, k0, nk, shift;                 // first query row (packed), queries here, first key row, keys, nk - nq
+    int i0;                                      // index of the first query in its sequence
+    int n[2];                                    // key tiles of each query tile
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int R>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
+template <int R>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_expanded_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap,
+                           const __grid_constant__ ExpandedArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, b = blockIdx.z;
+    volatile int* abort_flag = &sm.abort;
+
+    // The longest query tiles of a causal sequence first.
+    Plan p;
+    {
+        const int qs = a.q_start[b], qe = a.q_start[b + 1], ks = a.k_start[b], ke = a.k_start[b + 1];
+        const bool inside = qs >= 0 && qe >= qs && qe <= a.T && ks >= 0 && ke >= ks && ke <= a.S;
+        const int nq = inside ? qe - qs : 0;
+        if ((!inside || nq > a.max_q) && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) report(a.status, LSA_ERR_DEVICE_DATA);
+        const int todo = min(nq, a.max_q);
+        p.i0 = ((todo + 2 * kM - 1) / (2 * kM) - 1 - (int)blockIdx.x) * 2 * kM;
+        if (p.i0 < 0) return;                    // the whole CTA, before any barrier
+        p.q0 = qs + p.i0;
+        p.rows = min(2 * kM, todo - p.i0);
+        p.k0 = ks;
+        p.nk = ke - ks;
+        p.shift = p.nk - nq;
+        for (int t = 0; t < 2; ++t) {
+            const int r = min(kM, p.rows - t * kM);               // rows of the tile
+            const int end = r <= 0 ? 0 : (a.causal ? min(p.nk, max(0, p.i0 + t * kM + r + p.shift)) : p.nk);
+            p.n[t] = (end + kN - 1) / kN;
         }
     }
+    const int n_tiles = max(p.n[0], p.n[1]);
+    const bool partial = n_tiles * kN > p.nk;    // the last key tile reaches behind the sequence
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kUnits; ++i) {
+            tc::mbar_init(&sm.full[i], 1);
+            tc::mbar_init(&sm.empty[i], 1);
+        }
+        tc::mbar_init(&sm.q_full, 1);
+        tc::mbar_init(&sm.v_last[0], 1);
+        tc::mbar_init(&sm.v_last[1], 1);
+        tc::mbar_init(&sm.mma_done, 1);
+        for (int t = 0; t < 2; ++t) {
+            tc::mbar_init(&sm.s_full[t], 1);
+            tc::mbar_init(&sm.p_full[t][0], 4);
+            tc::mbar_init(&sm.p_full[t][1], 4);
+            tc::mbar_init(&sm.o_done[t], 1);
+        }
+        sm.abort = 0;
+        tc::fence_barrier_init();
+    }
+    if (warp == 8) tc::tmem_alloc(&sm.tmem_base, 512);
+    tc::tc_fence_before();
     __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    if (warp >= 8) {
+        reg_dec<kOtherRegs>();
+        if (warp == 9) {
+            // ---------------- TMA loads: Q, then the ring's units in the order of their use
+            if (tc::elect_one() && n_tiles > 0) {
+                const int hq = a.qh ? h : 0, hk = a.kh ? h : 0, hv = a.vh ? h : 0;   // a broadcast head has no stride
+                const int n_q = p.rows > kM ? 2 : 1;
+                tc::mbar_expect_tx(&sm.q_full, n_q * 3 * kM * 128);
+                for (int t = 0; t < n_q; ++t)
+                    for (int c = 0; c < 3; ++c)
+                        tc::tma_load_3d(sm.q[t][c], &qmap, &sm.q_full, c * 64, hq, p.q0 + t * kM);
+                int u = 0, issued = 0;
+                for (int j = 0; j < n_tiles; ++j) {
+                    const int row = p.k0 + j * kN;
+                    bool ok = true;
+                    for (int c = 0; c < kPerTile; ++c, ++u) {
+                        const int s = u % kUnits;
+                        if (!tc::mbar_wait(&sm.empty[s], ((u / kUnits) + 1) & 1, abort_flag)) { ok = false; break; }
+                        // The V units of a partial last tile pass through warp 10, which then completes `full`.
+                        uint64_t* bar = c >= 3 && partial && j == n_tiles - 1 ? &sm.v_last[c - 3] : &sm.full[s];
+                        tc::mbar_expect_tx(bar, kUnitBytes);
+                        if (c < 2) tc::tma_load_3d(sm.ring[s], &kmap, bar, c * 64, hk, row);
+                        else if (c == 2) tc::tma_load_2d(sm.ring[s], &rmap, bar, 0, row);
+                        else {
+                            tc::tma_load_3d(sm.ring[s], &vmap, bar, 0, hv, row + (c - 3) * 64);
+                            tc::tma_load_3d(sm.ring[s] + 8192, &vmap, bar, 64, hv, row + (c - 3) * 64);
+                        }
+                        issued = u + 1;
+                    }
+                    if (!ok) break;
+                }
+                // No copy outlives the CTA: every unit issued has landed (at once unless a wait gave up).
+                volatile int drain = 0;
+                tc::mbar_wait(&sm.q_full, 0, &drain);
+                for (int v = max(0, issued - kUnits); v < issued; ++v) {
+                    const int c = v % kPerTile;
+                    if (c >= 3 && partial && v / kPerTile == n_tiles - 1) tc::mbar_wait(&sm.v_last[c - 3], 0, &drain);
+                    else tc::mbar_wait(&sm.full[v % kUnits], (v / kUnits) & 1, &drain);
+                }
+            }
+        } else if (warp == 8) {
+            // ---------------- MMA issuer
+            const uint32_t idesc_s = tc::idesc_f16(kM, kN, 1), idesc_o = tc::idesc_f16_bmn(kM, kDv, 1);
+            if (tc::elect_one() && n_tiles > 0 && tc::mbar_wait(&sm.q_full, 0, abort_flag)) {
+                bool ok = true;
+                auto unit = [&](int j, int c) { return (j * kPerTile + c) % kUnits; };
+                auto landed = [&](int j, int c) {
+                    const int u = j * kPerTile + c;
+                    ok = ok && tc::mbar_wait(&sm.full[u % kUnits], (u / kUnits) & 1, abort_flag);
+                };
+                auto score = [&](int t, int j) {             // S_t = Q_t K_j^T
 #pragma unroll
-    for (int r = 0; r < kQ; ++r) {
-        if (r >= n) continue;
-        const float l = s.l[r], inv = l > 0.f ? 1.f / l : 0.f;
-        const size_t row = (size_t)(qs + i0 + r) * a.H + h;
-        if (a.o_f32) static_cast<float*>(a.o)[row * kDv + tid] = acc[r] * inv;
-        else static_cast<__nv_bfloat16*>(a.o)[row * kDv + tid] = __float2bfloat16_rn(acc[r] * inv);
-        if (tid == 0 && a.lse) a.lse[row] = l > 0.f ? (s.m[r] + log2f(l)) * 0.69314718055994530942f : kNegInf;
+                    for (int c = 0; c < 3; ++c) {
+                        landed(j, c);
+                        if (!ok) return;
+                        const uint32_t qa = tc::smem_u32(sm.q[t][c]), ka = tc::smem_u32(sm.ring[unit(j, c)]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_f16_ss(tmem + t * kN, tc::sdesc_sw128(qa + k * 32), tc::sdesc_sw128(ka + k * 32),
+                                           idesc_s, (c | k) != 0);
+                    }
+                    tc::mma_commit(&sm.s_full[t]);
+                };
+                auto weigh = [&](int t, int j) {             // O_t += P_t V_j
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        landed(j, 3 + hf);
+                        ok = ok && tc::mbar_wait(&sm.p_full[t][hf], j & 1, abort_flag);
+                        if (!ok) return;
+                        tc::tc_fence_after();
+                        const uint32_t va = tc::smem_u32(sm.ring[unit(j, 3 + hf)]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_f16_ts(tmem + 256 + t * kDv, tmem + t * kN + hf * 32 + k * 8,
+                                           tc::sdesc_sw128_lbo(va + k * 2048, 8192, 1024), idesc_o, (j | hf | k) != 0);
+                    }
+                    if (j == p.n[t] - 1) tc::mma_commit(&sm.o_done[t]);
+                };
+                auto release = [&](int j, int c0, int c1) {
+                    for (int c = c0; c < c1; ++c) tc::mma_commit(&sm.empty[unit(j, c)]);
+                };
+                if (p.n[0] > 0) score(0, 0);
+                if (ok && p.n[1] > 0) score(1, 0);
+                if (ok) release(0, 0, 3);
+                for (int j = 0; j < n_tiles && ok; ++j) {
+                    if (j < p.n[0]) weigh(0, j);
+                    if (ok && j + 1 < p.n[0]) score(0, j + 1);
+                    if (ok && j < p.n[1]) weigh(1, j);
+                    if (ok) release(j, 3, 5);
+                    if (ok && j + 1 < p.n[1]) score(1, j + 1);
+                    if (ok && j + 1 < n_tiles) release(j + 1, 0, 3);
+                }
+                // Drain before TMEM is freed: a commit completes after every MMA issued.
+                volatile int drain = 0;
+                if (!ok) *abort_flag = 1;
+                tc::mma_commit(&sm.mma_done);
+                tc::mbar_wait(&sm.mma_done, 0, &drain);
+            }
+        } else if (warp == 10 && partial && n_tiles > 0) {
+            // ---------------- rows of the last tile behind the sequence: zero
+            const int j = n_tiles - 1, from = p.nk - j * kN;
+            for (int hf = 0; hf < 2; ++hf) {
+                if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.v_last[hf], 0, abort_flag))) break;
+                const int s = (j * kPerTile + 3 + hf) % kUnits, r0 = max(0, from - hf * 64);
+                for (int i = lane; i < (64 - min(64, r0)) * 16; i += 32)
+                    *reinterpret_cast<uint4*>(sm.ring[s] + ((i >> 3) & 1) * 8192 + (r0 + (i >> 4)) * 128 + (i & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.full[s]);
+            }
+        }
+    } else {
+        reg_inc<kSoftmaxRegs>();
+        // ---------------- softmax and epilogue: thread = query row
+        const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_col = tmem + t * kN + lane_off, o_col = tmem + 256 + t * kDv + lane_off;
+        const int n = p.n[t], i = p.i0 + t * kM + row;
+        const bool live = t * kM + row < p.rows;
+        const int lim = a.causal ? min(p.nk, max(0, i + 1 + p.shift)) : p.nk;     // keys this row sees
+        const float sc = a.sm_scale_log2;
+        float m = kNegInf, l = 0.f;                  // reference maximum (log2 units) and sum
+        bool alive = true;
+        for (int j = 0; j < n; ++j) {
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[t], j & 1, abort_flag))) { alive = false; break; }
+            tc::tc_fence_after();
+            uint32_t w[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, w[c]);
+            tc::tmem_wait_ld();
+            const int left = lim - j * kN;           // keys of this tile that the row sees
+            if (__any_sync(0xffffffffu, left < kN)) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e >= left) w[c][e] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                mx[c] = __uint_as_float(w[c][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(w[c][e]));
+            }
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            // The reference rises only when the tile exceeds it by more than 2^8; weights stay below 2^8.
+            float alpha = 1.f;
+            bool rescale = false;
+            if (mt > m + 8.f) {
+                if (m != kNegInf) { alpha = ex2(m - mt); rescale = true; }
+                l *= alpha;
+                m = mt;
+            }
+            if (__any_sync(0xffffffffu, rescale)) {  // O holds P V of the tiles before: their MMAs precede this S
+#pragma unroll 1
+                for (int c = 0; c < kDv / 32; ++c) {
+                    uint32_t ov[32];
+                    tc::tmem_ld32(o_col + c * 32, ov);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                    tc::tmem_st32(o_col + c * 32, ov);
+                }
+            }
+            const float mref = m == kNegInf ? 0.f : m;
+            const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-mref, -mref);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t pw[32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint32_t* s2 = &w[2 * hf + c][e];
+                        float2 x = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])), sc2, m2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[(e >> 1) & 1].x += x.x;
+                        sum[(e >> 1) & 1].y += x.y;
+                        pw[c * 16 + e / 2] = pack_bf16x2(x.x, x.y);
+                    }
+                tc::tmem_st32(s_col + hf * 32, pw);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.p_full[t][hf]);
+            }
+            l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        }
+        if (n > 0 && alive) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_done[t], 0, abort_flag));
+        tc::tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const size_t orow = (size_t)(p.q0 + t * kM + row) * a.H + h;
+#pragma unroll 1
+        for (int c = 0; c < kDv / 32; ++c) {
+            uint32_t ov[32];
+            if (n > 0 && alive) {
+                tc::tmem_ld32(o_col + c * 32, ov);
+                tc::tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = 0u;
+            }
+            __syncwarp();
+            if (live) {
+                float f[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                if (a.o_f32) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kDv + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                            pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                }
+            }
+            __syncwarp();
+        }
+        if (live && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
     }
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    if (sm.abort && threadIdx.x == 0) report(a.status, LSA_ERR_TIMEOUT);
+    if (warp == 8) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// [tokens][heads][dims] BF16 as a 3-D tensor, box 64 dims x 1 head x `rows` tokens, 128-byte swizzle.  A dimension of
+// one element, or a broadcast one (stride 0, taken at coordinate 0), has extent 1 and any valid stride.
+bool make_map(CUtensorMap* m, const uint16_t* base, int dims, int heads, int64_t head_stride, int tokens,
+              int64_t tok_stride, int rows) {
+    const bool one = heads == 1 || head_stride == 0;
+    const cuuint64_t d[3] = {(cuuint64_t)dims, (cuuint64_t)(one ? 1 : heads), (cuuint64_t)tokens};
+    const cuuint64_t s[2] = {(cuuint64_t)(one ? dims : head_stride) * 2, (cuuint64_t)(tok_stride ? tok_stride : dims) * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
+    const cuuint32_t e[3] = {1, 1, 1};
+    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), d, s, box, e,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_latent_expanded(const ExpandedArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(latent_expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (tc::encode_tiled() == nullptr) return cudaErrorNotSupported;
+    CUtensorMap qm, km, rm, vm;
+    memset(&km, 0, sizeof(km));
+    memset(&rm, 0, sizeof(rm));
+    memset(&vm, 0, sizeof(vm));
+    if (!make_map(&qm, a.q, kD, a.H, a.qh, a.T, a.qt, kM)) return cudaErrorInvalidValue;
+    if (a.S > 0) {
+        const cuuint64_t d[2] = {kDr, (cuuint64_t)a.S}, s[1] = {(cuuint64_t)(a.rt ? a.rt : kDr) * 2};
+        const cuuint32_t box[2] = {64, kN}, e[2] = {1, 1};
+        if (!make_map(&km, a.kn, kDn, a.H, a.kh, a.S, a.kt, kN) || !make_map(&vm, a.v, kDv, a.H, a.vh, a.S, a.vt, 64) ||
+            tc::encode_tiled()(&rm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(a.kr), d, s, box, e,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const size_t smem = sizeof(Smem) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(latent_expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    latent_expanded_kernel<<<dim3((a.max_q + kQ - 1) / kQ, a.H, a.B), kThreads, sizeof(Smem), st>>>(a);
+    latent_expanded_kernel<<<dim3((a.max_q + 2 * kM - 1) / (2 * kM), a.H, a.B), kThreads, smem, st>>>(qm, km, rm, vm, a);
     return cudaGetLastError();
 }
 
