@@ -294,7 +294,7 @@ lsa_status lsa_rope_apply(const lsa_rope* r, int T, int H, int D, int rope_off, 
  * data + i * seq_stride (scale + i * scale_seq_stride) -- the lsa_cache's "sequences" are the pages.  Calls
  * that take an lsa_pages accept NULL for a cache without pages.  Entries past a sequence's last position are
  * never read; an entry that is read and lies outside 0 .. n_pages - 1 is bad device data, and its rows are
- * skipped (lsa_cache_append) or read as masked (attention). */
+ * skipped (lsa_cache_append) or read as zeros (attention). */
 typedef struct {
     const int32_t* table;          /* device [B][ld] */
     int64_t        ld;             /* entries between sequences, >= pages_per_seq */

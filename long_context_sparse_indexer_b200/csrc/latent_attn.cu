@@ -1,141 +1,952 @@
-// Latent attention in the absorbed form over every visible cached row, paged or not.
+// Latent attention in the absorbed form over every visible cached row, paged or not, on the 5th-generation
+// tensor cores.
 //
-//   z_s = sm_scale q . K_s (576), o = softmax(z) V (V = the first 512 elements of the same row).
+//   z_s = sm_scale q . K_s (576), o = softmax(z) V (V = the first 512 elements of the same row), one pass with a
+//   running reference maximum and sum.
 //
-// One pass with a running maximum and sum.  Block = (16 heads, token): the heads' queries in shared memory
-// as FP32, rows brought in tiles of 16 and widened, each thread two of the 16 x 16 scores, then each thread
-// 4 dimensions of all 16 heads' accumulators in registers.  CUDA cores, FP32 throughout: bound by them.
+// Units and cut.  The rows of a group (q_group tokens x H heads, one sequence) are taken 128 at a time: a unit,
+// whose work is ceil(longest context of its tokens / 64) key tiles.  The tiles of all units, laid end to end, are
+// cut into equal runs, one per cluster, so ragged lengths and few tokens load the GPU evenly.  A unit that lies
+// in one run is written out; one that is cut leaves FP32 partial results (at most two per cluster), joined by
+// latent_merge_kernel.  The cut depends on the inputs only, so results repeat bit for bit.
+//
+// A cluster is two CTAs and one tcgen05 pair (cta_group::2, M = 128): CTA c holds rows [64 c, 64 c + 64) of the
+// unit, on TMEM lanes 0..63 for the first half of each product's columns and 64..127 for the second, so the
+// 64 x 512 FP32 accumulator takes 256 columns and leaves room for scores and queries; a single CTA with 128 rows
+// would need all 512.  The pair runs at the full rate of both tensor cores (measured: 64 cycles for M = 128,
+// N = 256, K = 16).  Of a key tile's 64 keys CTA c loads its own 32 whole, as its half of the B operand of the
+// scores; for P V it needs the other 32 as well, in its 256 value dimensions: once the scores are done these are
+// loaded over the 256 dimensions of its own keys that only the scores needed.  Every byte crosses to an SM once
+// for S and half of them once more for V, against twice the rows for a pair of independent CTAs.
+//
+// Memory.  TMEM: O [0, 256), two score buffers [256, 320), Q dims 0..383 [320, 512) (each row on lanes r and
+// r + 64; a query operand from TMEM spares the shared-memory port, which S alone would fill: 4 KB per 32-cycle
+// MMA).  Shared memory: Q dims 384..575, two P buffers (BF16), a ring of five 36 KB stages; a stage is nine
+// 64-dim atoms of 32 keys, atoms 0..3 / 4..7 doubling as the value rows of keys 0..31 / 32..63.  Queries arrive
+// through two stages of the same ring.
+//
+// Warps: 0..3 softmax (thread = TMEM lane = (row, half of the keys); the two halves of a row exchange their
+// maxima through shared memory), 4 the MMAs (in CTA 0, for both), 5 the plan of the cluster's segments.  BF16:
+// 6 and 7 load keys and values by TMA, one box per tile for pages of whole 32 rows.  FP8: warps 6..11 and 12..15
+// load codes and widen them to BF16 on the way to the same stages (bit moves and one exact multiply a pair).
+// All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
+#include <cstring>
+#include <mutex>
 
 #include "kernels.cuh"
+#include "tc.cuh"
 
 namespace lsa {
 
 namespace {
 
-constexpr int kThreads = 128, kHeads = 16, kRows = 16, kD = 576, kDv = 512;
+constexpr int kD = 576, kDv = 512, kM = 128, kRows = 64;         // unit rows, rows of a CTA
+constexpr int kTile = 64, kOwn = 32;                             // keys of a tile, of a CTA
+constexpr int kStages = 5, kAtoms = 9, kAtomBytes = kOwn * 128, kStageBytes = kAtoms * kAtomBytes;
+constexpr int kXBytes = 4 * kAtomBytes;
+constexpr int kQTmem = 6;                                        // query atoms in TMEM, the others in shared memory
+constexpr int kSCol = 256, kQCol = 320;
+constexpr int kSegs = 3;                                         // published segments
+constexpr int kMaxClusters = 80;
+constexpr int kKWarps = 6, kXWarps = 4;                          // FP8 converters
+static_assert(kQCol + kQTmem * 32 == 512, "TMEM columns");
 
-struct Smem {
-    float q[kHeads][kD + 1];
-    float k[kRows][kD + 1];
-    float p[kHeads][kRows];
-    float m[kHeads], l[kHeads], alpha[kHeads];
-    int64_t row[kRows];                          // byte offset of each row, or -1
-    float scale[kRows];
+struct Seg {
+    int unit, seq, k0, k1, n, len;               // key tiles [k0, k1) of the unit's n; keys below len; unit < 0: the end
 };
 
-__global__ void __launch_bounds__(kThreads) latent_attn_kernel(LatentArgs a) {
-    extern __shared__ uint8_t raw[];
-    Smem& s = *reinterpret_cast<Smem*>(raw);
-    const int t = blockIdx.x, h0 = blockIdx.y * kHeads, tid = threadIdx.x;
-    const int nh = min(kHeads, a.H - h0);
-    const int g0 = t / a.q_group * a.q_group;
-    const int b = a.q_seq[g0], pos = a.q_pos[t];
-    int n = 0;
-    if (pos >= 0) {
-        const bool ok = b >= 0 && b < a.B && a.q_seq[t] == b && pos < a.seq_len[b] && a.seq_len[b] <= a.L_alloc;
-        if (ok) n = pos + 1;
-        else if (tid == 0) report(a.status, LSA_ERR_DEVICE_DATA);
+struct Smem {
+    alignas(1024) uint8_t ring[kStages][kStageBytes];
+    alignas(1024) uint8_t q[kAtoms - kQTmem][kRows * 128];
+    alignas(1024) uint8_t p[2][kRows * 128];
+    float kscale[kStages][kTile];                // FP8: the tile's row scales
+    float mx[2][128];                            // what the halves of a row exchange: tile maxima, sums
+    Seg seg[kSegs];
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
+    uint64_t k_full[kStages];                    // CTA 0: both CTAs' keys have landed
+    uint64_t sc_full[kStages];                   // FP8: kscale is written
+    uint64_t x_go[kStages], x_full[kStages];     // the scores of the stage are done; its exchanged rows have landed
+    uint64_t empty[kStages];
+    uint64_t q_full, q_ready;                    // queries staged; (CTA 0) moved to their operand places in both CTAs
+    uint64_t s_full[2], s_free[2];               // scores done; (CTA 0) read by both CTAs
+    uint64_t p_full[2], pv_done[2];              // (CTA 0) weights and value rows in place; their product done
+    uint64_t pair[2];                            // softmax warps w and w + 2: the halves' values are written
+    uint64_t q_taken;                            // every softmax warp has read the staged queries
+    uint64_t mma_done;
+    long long scan[32];
+    long long total;
+    int u0, k0;                                  // where the cluster's run starts
+    uint32_t tmem_base;
+    int abort;
+};
+
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
+
+// Workspace: a header, then the partial results of 2 kMaxClusters slots.
+struct WsHeader {
+    int clusters;                                // runs of this call
+    int unit[kMaxClusters], k0[kMaxClusters];    // each run's first unit and tile in it
+};
+constexpr size_t kWsO = 4096;
+constexpr size_t kWsLse = kWsO + (size_t)2 * kMaxClusters * kM * kDv * 4;
+constexpr size_t kWsBytes = kWsLse + (size_t)2 * kMaxClusters * kM * 4;
+static_assert(sizeof(WsHeader) <= kWsO, "header");
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---- pair forms of the tcgen05 and mbarrier operations
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t n) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(tc::smem_u32(dst)), "r"(n) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t t, uint32_t n) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(t), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA issued so far has completed.
+__device__ __forceinline__ void commit2(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(tc::smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+// Release-arrive on a barrier of CTA 0.
+__device__ __forceinline__ void arrive0(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(tc::peer_smem(bar, 0)) : "memory");
+}
+// 4-D box into this CTA's shared memory, completing on the barrier at shared::cluster address bar of the pair's CTA 0.
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 4-D box completing on a barrier of this CTA.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Four e4m3 codes (a word) to BF16, exactly: the code's exponent and mantissa moved into a BF16's make
+// value * 2^-120 (subnormals included), one multiply by 2^120 restores it.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    uint2 r;
+    const uint32_t t0 = __byte_perm(w, 0, 0x1404), t1 = __byte_perm(w, 0, 0x3424);
+    const uint32_t u0 = (t0 & 0x80008000u) | ((t0 >> 4) & 0x07f007f0u), u1 = (t1 & 0x80008000u) | ((t1 >> 4) & 0x07f007f0u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(u0), "r"(0x7b807b80u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(u1), "r"(0x7b807b80u));
+    return r;
+}
+
+struct LatentKernelArgs {
+    LatentArgs a;
+    int units, m_tiles, group_rows;              // units, units of a group, rows of a group
+    int clusters, box_rows;
+};
+
+// Keys that some token of the unit sees (0: padding only), and its sequence.  `tell`: report bad tokens.
+__device__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
+    const LatentArgs& a = k.a;
+    const int g = u / k.m_tiles, r0 = (u - g * k.m_tiles) * kM, r1 = min(k.group_rows, r0 + kM);
+    const int t0 = g * a.q_group, b = a.q_seq[t0];
+    int sl = 0;
+    if (b >= 0 && b < a.B) {
+        sl = a.seq_len[b];
+        if (sl > a.L_alloc) sl = 0;
     }
-    for (int i = tid; i < kHeads * kD; i += kThreads) {
-        const int h = i / kD, d = i % kD;
-        s.q[h][d] = h < nh ? bf16_bits_to_float(a.q[((size_t)t * a.H + h0 + h) * kD + d]) * a.sm_scale_log2 : 0.f;
+    *seq = b;
+    int len = 0;
+    bool bad = false;
+    for (int t = t0 + r0 / a.H; t <= t0 + (r1 - 1) / a.H; ++t) {
+        const int pos = a.q_pos[t];
+        if (pos < 0) continue;
+        if (pos < sl && a.q_seq[t] == b) len = max(len, pos + 1);
+        else bad = true;
     }
-    if (tid < kHeads) { s.m[tid] = kNegInf; s.l[tid] = 0.f; }
-    float acc[kHeads][4];
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
-    for (int r0 = 0; r0 < n; r0 += kRows) {
-        __syncthreads();
-        if (tid < kRows) {
-            const int r = r0 + tid;
-            int64_t off = -1;
-            float sc = 1.f;
-            if (r < n) {
-                int64_t lead = b, row = r;
-                if (a.table) {
-                    const int pg = r / a.page_size;
-                    row = r - pg * a.page_size;
-                    lead = a.table[b * a.table_ld + pg];
-                }
-                if (lead >= 0 && lead < a.n_pages) {
-                    off = lead * a.seq_b + row * a.tok_b;
-                    if (a.kv_scale) sc = a.kv_scale[lead * a.scale_seq + row];
-                } else report(a.status, LSA_ERR_DEVICE_DATA);
-            }
-            s.row[tid] = off;
-            s.scale[tid] = sc;
+    if (bad && tell) report(a.status, LSA_ERR_DEVICE_DATA);
+    return len;
+}
+
+template <bool FP8>
+constexpr int kThreadsOf = FP8 ? 32 * (6 + kKWarps + kXWarps) : 32 * 8;
+
+template <bool FP8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap xmap, const __grid_constant__ LatentKernelArgs k) {
+    constexpr int kThreads = kThreadsOf<FP8>;
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const LatentArgs& a = k.a;
+    const int rank = blockIdx.x & 1, cluster = blockIdx.x >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &sm.abort;
+
+    if (threadIdx.x == 0) {
+        constexpr int kLoaders = FP8 ? kKWarps + kXWarps : 2;
+        for (int i = 0; i < kSegs; ++i) {
+            tc::mbar_init(&sm.seg_full[i], 1);
+            tc::mbar_init(&sm.seg_empty[i], 4 + kLoaders + (rank == 0 ? 1 : 0));
         }
-        __syncthreads();
-        for (int i = tid; i < kRows * kD; i += kThreads) {
-            const int r = i / kD, d = i % kD;
-            float v = 0.f;
-            if (s.row[r] >= 0) {
-                const uint8_t* p = a.kv + s.row[r];
-                if (a.kv_scale) v = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(p[d]) & 0xffff))) * s.scale[r];
-                else v = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[d]);
-            }
-            s.k[r][d] = v;
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&sm.k_full[i], FP8 ? 2 * kKWarps : 1);
+            tc::mbar_init(&sm.sc_full[i], 1);
+            tc::mbar_init(&sm.x_go[i], 1);
+            tc::mbar_init(&sm.x_full[i], FP8 ? kXWarps : 1);
+            tc::mbar_init(&sm.empty[i], 1);
         }
-        __syncthreads();
-        for (int i = tid; i < kHeads * kRows; i += kThreads) {
-            const int h = i / kRows, r = i % kRows;
-            float z = 0.f;
-            for (int d = 0; d < kD; ++d) z = fmaf(s.q[h][d], s.k[r][d], z);
-            s.p[h][r] = s.row[r] >= 0 ? z : kNegInf;
+        tc::mbar_init(&sm.q_full, 1);
+        tc::mbar_init(&sm.q_ready, 8);
+        tc::mbar_init(&sm.q_taken, 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.s_full[i], 1);
+            tc::mbar_init(&sm.s_free[i], 8);
+            tc::mbar_init(&sm.p_full[i], 8);
+            tc::mbar_init(&sm.pv_done[i], 1);
+            tc::mbar_init(&sm.pair[i], 2);
         }
-        __syncthreads();
-        if (tid < kHeads) {
-            float m = s.m[tid];
-            for (int r = 0; r < kRows; ++r) m = fmaxf(m, s.p[tid][r]);
-            const float ref = m == kNegInf ? 0.f : m;
-            const float al = exp2f(s.m[tid] - ref);
-            float l = s.l[tid] * al;
-            for (int r = 0; r < kRows; ++r) {
-                s.p[tid][r] = exp2f(s.p[tid][r] - ref);
-                l += s.p[tid][r];
-            }
-            s.m[tid] = m; s.l[tid] = l; s.alpha[tid] = al;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            const float al = s.alpha[h];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = acc[h][e] * al;
-                for (int r = 0; r < kRows; ++r) v = fmaf(s.p[h][r], s.k[r][tid + e * kThreads], v);
-                acc[h][e] = v;
-            }
-        }
+        tc::mbar_init(&sm.mma_done, 1);
+        sm.abort = 0;
+        tc::fence_barrier_init();
     }
+    if (warp == 4) tmem_alloc2(&sm.tmem_base, 512);
+
+    // The plan: tiles per unit, summed over the block; each thread takes a run of units.
+    const int per = (k.units + kThreads - 1) / kThreads;
+    const int ua = min(k.units, (int)threadIdx.x * per), ub = min(k.units, ua + per);
+    long long mine = 0;
+    for (int u = ua; u < ub; ++u) {
+        int seq;
+        mine += (unit_len(k, u, &seq, blockIdx.x == 0) + kTile - 1) / kTile;
+    }
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) sm.scan[warp] = before;
     __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sm.scan[w];
+        total += sm.scan[w];
+    }
+    before -= mine;
+    const int n_runs = (int)min((long long)k.clusters, total);
+    const long long lo = n_runs ? total * cluster / n_runs : 0, hi = n_runs ? total * (cluster + 1) / n_runs : 0;
+    const bool busy = cluster < n_runs;
+    if (busy && before <= lo && lo < before + mine) {              // one thread: the run starts among its units
+        long long at = before;
+        for (int u = ua; u < ub; ++u) {
+            int seq;
+            const int n = (unit_len(k, u, &seq, false) + kTile - 1) / kTile;
+            if (lo < at + n) {
+                sm.u0 = u;
+                sm.k0 = (int)(lo - at);
+                if (rank == 0) {
+                    WsHeader* w = static_cast<WsHeader*>(a.ws);
+                    w->unit[cluster] = u;
+                    w->k0[cluster] = sm.k0;
+                }
+                break;
+            }
+            at += n;
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) static_cast<WsHeader*>(a.ws)->clusters = n_runs;
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync_all();                      // both CTAs' barriers and TMEM exist
+    tc::tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    // Segments, as every role but warp 5 takes them.
+    int seg_i = 0;
+    auto next_seg = [&](Seg& s) -> bool {
+        const int d = seg_i % kSegs;
+        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.seg_full[d], (seg_i / kSegs) & 1, abort_flag));
+        s = sm.seg[d];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.seg_empty[d]);
+        ++seg_i;
+        return ok && s.unit >= 0;
+    };
+    // Byte offset of a sequence's row (pages or not), or -1 for a page outside the pool.
+    auto page_of = [&](int seq, int row, int* in_page) -> int {
+        if (!a.table) { *in_page = row; return seq; }
+        const int pg = row / a.page_size;
+        *in_page = row - pg * a.page_size;
+        const int id = a.table[seq * a.table_ld + pg];
+        if (id >= 0 && id < a.n_pages) return id;
+        report(a.status, LSA_ERR_DEVICE_DATA);
+        return -1;
+    };
+
+    // Queries of a segment into the two stages at ring position r (one warp).  The segment before must have taken
+    // its own: their barrier counts one phase at a time.
+    auto load_q = [&](const Seg& s, int r, int seg) -> bool {
+        const int g = s.unit / k.m_tiles, q0 = g * k.group_rows + (s.unit - g * k.m_tiles) * kM + rank * kRows;
+        bool ok = seg == 0 || __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_taken, (seg - 1) & 1, abort_flag));
+        for (int i = 0; i < 2 && ok; ++i) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[(r + i) % kStages], (((r + i) / kStages) + 1) & 1, abort_flag));
+            if (ok && lane == 0) {
+                if (i == 0) tc::mbar_expect_tx(&sm.q_full, 2 * kStageBytes);
+                tc::tma_load_3d(sm.ring[(r + i) % kStages], &qmap, &sm.q_full, 0, q0 + i * 32, 0);
+            }
+        }
+        return ok;
+    };
+
+    if (warp == 5) {
+        // ---------------- plan: the run's segments, then the units that hold padding only
+        if (busy) {
+            int seg = 0, u = sm.u0, k0 = sm.k0;
+            long long left = hi - lo;
+            bool ok = true;
+            while (ok && left > 0) {
+                // 32 units at a time.
+                int seq = 0;
+                const int len = u + lane < k.units ? unit_len(k, u + lane, &seq, false) : 0;
+                for (int i = 0; i < 32 && left > 0 && u + i < k.units; ++i) {
+                    Seg s;
+                    s.unit = u + i;
+                    s.len = __shfl_sync(0xffffffffu, len, i);
+                    s.seq = __shfl_sync(0xffffffffu, seq, i);
+                    s.n = (s.len + kTile - 1) / kTile;
+                    if (s.n == 0) continue;
+                    s.k0 = k0;
+                    s.k1 = (int)min((long long)s.n, s.k0 + left);
+                    k0 = 0;
+                    left -= s.k1 - s.k0;
+                    const int d = seg % kSegs;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        sm.seg[d] = s;
+                        tc::mbar_arrive(&sm.seg_full[d]);
+                    }
+                    ++seg;
+                }
+                u += 32;
+                if (u >= k.units) break;
+            }
+            const int d = seg % kSegs;
+            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
+            if (ok && lane == 0) {
+                sm.seg[d].unit = -1;
+                tc::mbar_arrive(&sm.seg_full[d]);
+            }
+        }
+        for (int u0 = blockIdx.x; u0 < k.units; u0 += 32 * gridDim.x) {
+            int seq;
+            const int u = u0 + lane * gridDim.x;
+            unsigned none = __ballot_sync(0xffffffffu, u < k.units && unit_len(k, u, &seq, false) == 0);
+            for (; none; none &= none - 1) {
+                const int v = u0 + (__ffs(none) - 1) * gridDim.x, g = v / k.m_tiles, r0 = (v - g * k.m_tiles) * kM;
+                const size_t row = (size_t)g * k.group_rows + r0;
+                const int n = min(k.group_rows - r0, kM), eb = a.o_f32 ? 4 : 2;
+                uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.o) + row * kDv * eb);
+                for (int i = lane; i < n * kDv * eb / 16; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+                if (a.lse)
+                    for (int i = lane; i < n; i += 32) a.lse[row + i] = kNegInf;
+            }
+        }
+    } else if (busy && warp == 4) {
+        // ---------------- MMA issuer (CTA 0)
+        if (rank == 0) {
+            const uint32_t idesc_s = tc::idesc_f16(128, kTile, 1), idesc_o = tc::idesc_f16_bmn(128, 256, 1);
+            int r = 0, tile = 0, seg = 0;        // ring position, key tiles so far, segments so far
+            uint32_t k_ph = 0;                   // parity of each stage's next keys
+            const bool leader = tc::elect_one();
+            bool ok = true, any = false;
+            Seg s;
+            while (ok && next_seg(s)) {
+                r += 2;                          // the queries' stages
+                const int n = s.k1 - s.k0;
+                if (leader) {
+                    ok = tc::mbar_wait_cluster(&sm.q_ready, seg & 1, abort_flag);
+                    auto score = [&](int i) {
+                        const int st = (r + i) % kStages, bf = (tile + i) & 1;
+                        ok = ok && tc::mbar_wait_cluster(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
+                             tc::mbar_wait_cluster(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
+                        if (!ok) return;
+                        k_ph ^= 1u << st;
+                        tc::tc_fence_after();
+                        const uint32_t ka = tc::smem_u32(sm.ring[st]), qa = tc::smem_u32(sm.q[0]);
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-        if (h >= nh) continue;
-        const float l = s.l[h], inv = l > 0.f ? 1.f / l : 0.f;
-        const size_t row = (size_t)t * a.H + h0 + h;
+                        for (int at = 0; at < kAtoms; ++at)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint64_t bd = tc::sdesc_sw128(ka + at * kAtomBytes + kk * 32);
+                                if (at < kQTmem) mma2_ts(tmem + kSCol + bf * 32, tmem + kQCol + at * 32 + kk * 8, bd, idesc_s, (at | kk) != 0);
+                                else mma2_ss(tmem + kSCol + bf * 32, tc::sdesc_sw128(qa + (at - kQTmem) * (kRows * 128) + kk * 32), bd, idesc_s, 1u);
+                            }
+                        commit2(&sm.s_full[bf]);
+                        commit2(&sm.x_go[st]);
+                        any = true;
+                    };
+                    if (ok) score(0);
+                    if (ok && n > 1) score(1);
+                    for (int i = 0; i < n && ok; ++i) {
+                        if (i + 2 < n) score(i + 2);
+                        const int st = (r + i) % kStages, pb = (tile + i) & 1;
+                        ok = ok && tc::mbar_wait_cluster(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        const uint32_t va = tc::smem_u32(sm.ring[st]), pa = tc::smem_u32(sm.p[pb]);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t ad = tc::sdesc_sw128(pa + kk * 32);
+                            const uint32_t vk = va + (kk >> 1) * 4 * kAtomBytes + (kk & 1) * 2048;
+#pragma unroll
+                            for (int ob = 0; ob < 2; ++ob)
+                                mma2_ss(tmem + ob * 128, ad, tc::sdesc_sw128_lbo(vk + ob * 2 * kAtomBytes, kAtomBytes, 1024), idesc_o,
+                                        (i | kk) != 0);
+                        }
+                        commit2(&sm.empty[st]);
+                        commit2(&sm.pv_done[pb]);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                r += n;
+                tile += n;
+                ++seg;
+            }
+            if (leader && any) {                 // drain before TMEM is freed
+                volatile int drain = 0;
+                commit2(&sm.mma_done);
+                tc::mbar_wait_cluster(&sm.mma_done, 0, &drain);
+            }
+        }
+    } else if (busy && warp < 4) {
+        // ---------------- softmax: lane L of TMEM = row L & 63, keys 32 (L >> 6) .. + 31 of a tile
+        const int L = warp * 32 + lane, row = L & 63, hf = L >> 6;
+        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        int r = 0, tile = 0, seg = 0;
+        uint32_t x_ph = 0, sc_ph = 0;
+        bool alive = true;
+        Seg s;
+        // Queries of the next segment from the two stages at ring position r to their operand places.
+        auto take_q = [&](int r) {
+            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_full, seg & 1, abort_flag));
+            if (!alive) return;
+            const uint8_t* src = sm.ring[(r + (row >> 5)) % kStages] + (row & 31) * 128;
+#pragma unroll 2
+            for (int at = 0; at < kQTmem; ++at) {
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + at * kAtomBytes + ((c ^ (row & 7)) << 4));
+                    w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+                }
+                tc::tmem_st32(tmem + kQCol + at * 32 + lane_off, w);
+            }
+#pragma unroll
+            for (int at = kQTmem; at < kAtoms; ++at)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)      // the same swizzle: bytes move as they are
+                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + c) * 16) =
+                        *reinterpret_cast<const uint4*>(src + at * kAtomBytes + (4 * hf + c) * 16);
+            tc::fence_proxy_async_smem();
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(&sm.q_taken);
+                arrive0(&sm.q_ready);
+            }
+            if (warp == 0) {                     // the stages are free once every warp has read them
+                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_taken, seg & 1, abort_flag));
+                if (alive && lane == 0) {
+                    tc::mbar_arrive(&sm.empty[r % kStages]);
+                    tc::mbar_arrive(&sm.empty[(r + 1) % kStages]);
+                }
+            }
+        };
+        // The value of the other half of this row (its thread is in warp w ^ 2).
+        int swaps = 0;
+        auto swap = [&](float v) -> float {
+            const int bf = swaps & 1;
+            sm.mx[bf][L] = v;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.pair[warp & 1]);
+            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pair[warp & 1], swaps & 1, abort_flag));
+            ++swaps;
+            return sm.mx[bf][L ^ 64];
+        };
+        bool have = next_seg(s);
+        if (have) take_q(0);
+        while (have && alive) {
+            r += 2;
+            const int n = s.k1 - s.k0, g = s.unit / k.m_tiles, r0 = (s.unit - g * k.m_tiles) * kM + rank * kRows;
+            const int grow = r0 + row;           // row in the group
+            int lim = 0;                         // keys this row sees
+            if (grow < k.group_rows) {
+                const int t = g * a.q_group + grow / a.H, pos = a.q_pos[t];
+                if (pos >= 0 && a.q_seq[t] == s.seq && pos < a.seq_len[s.seq]) lim = pos + 1;
+            }
+            float m = kNegInf, l = 0.f;
+            for (int i = 0; i < n; ++i, ++r, ++tile) {
+                const int bf = tile & 1, st = r % kStages, key0 = (s.k0 + i) * kTile;
+                if (FP8) {
+                    alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sc_full[st], (sc_ph >> st) & 1, abort_flag));
+                    sc_ph ^= 1u << st;
+                    if (!alive) break;
+                }
+                alive = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.s_full[bf], (tile >> 1) & 1, abort_flag));
+                if (!alive) break;
+                tc::tc_fence_after();
+                uint32_t w[32];
+                tc::tmem_ld32(tmem + kSCol + bf * 32 + lane_off, w);
+                tc::tmem_wait_ld();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive0(&sm.s_free[bf]);
+                float x[32];
+                if constexpr (FP8) {
+                    const float4* ks = reinterpret_cast<const float4*>(&sm.kscale[st][hf * 32]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 v = ks[e];
+                        x[4 * e + 0] = __uint_as_float(w[4 * e + 0]) * (v.x * a.sm_scale_log2);
+                        x[4 * e + 1] = __uint_as_float(w[4 * e + 1]) * (v.y * a.sm_scale_log2);
+                        x[4 * e + 2] = __uint_as_float(w[4 * e + 2]) * (v.z * a.sm_scale_log2);
+                        x[4 * e + 3] = __uint_as_float(w[4 * e + 3]) * (v.w * a.sm_scale_log2);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(w[e]) * a.sm_scale_log2;
+                }
+                const int left = lim - key0 - hf * 32;
+                if (__any_sync(0xffffffffu, left < 32)) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e >= left) x[e] = kNegInf;
+                }
+                float mt = x[0];
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mt = fmaxf(mt, x[e]);
+                mt = fmaxf(mt, swap(mt));
+                if (!alive) break;
+                // The reference rises only when the tile exceeds it by more than 2^8 (both halves alike).
+                float alpha = 1.f;
+                bool rescale = false;
+                if (mt > m + 8.f) {
+                    if (m != kNegInf) { alpha = ex2(m - mt); rescale = true; }
+                    l *= alpha;
+                    m = mt;
+                }
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O must hold every product so far; P V of two tiles ago is known done, so the phase is unambiguous.
+                    if (i > 0) {
+                        alive = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.pv_done[bf ^ 1], ((tile - 1) >> 1) & 1, abort_flag));
+                        if (!alive) break;
+                    }
+                    tc::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 32) {
+                        uint32_t ov[32];
+                        tc::tmem_ld32(tmem + c + lane_off, ov);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tc::tmem_st32(tmem + c + lane_off, ov);
+                    }
+                    tc::tmem_wait_st();
+                }
+                const float mref = m == kNegInf ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pw[16];
+                const float4* vs = reinterpret_cast<const float4*>(&sm.kscale[st][hf * 32]);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float p0 = ex2(x[e] - mref), p1 = ex2(x[e + 1] - mref), p2 = ex2(x[e + 2] - mref), p3 = ex2(x[e + 3] - mref);
+                    sum[0] += p0; sum[1] += p1; sum[2] += p2; sum[3] += p3;
+                    if constexpr (FP8) {                           // the row's scale goes into its weight (a masked row's may be anything)
+                        const float4 v = vs[e / 4];
+                        p0 = p0 > 0.f ? p0 * v.x : 0.f;
+                        p1 = p1 > 0.f ? p1 * v.y : 0.f;
+                        p2 = p2 > 0.f ? p2 * v.z : 0.f;
+                        p3 = p3 > 0.f ? p3 * v.w : 0.f;
+                    }
+                    pw[e / 2] = pack_bf16x2(p0, p1);
+                    pw[e / 2 + 1] = pack_bf16x2(p2, p3);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                // P into its buffer once the product two tiles ago has read it, and not before the tile's value rows are there.
+                if (tile >= 2) alive = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.pv_done[bf], ((tile >> 1) - 1) & 1, abort_flag));
+                if (!alive) break;
+                uint8_t* prow = sm.p[bf] + row * 128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4*>(prow + (((4 * hf + c) ^ (row & 7)) << 4)) =
+                        make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_full[st], (x_ph >> st) & 1, abort_flag));
+                x_ph ^= 1u << st;
+                if (!alive) break;
+                if (!FP8 && key0 + kTile > s.len) {                // value rows behind the last key: zero
+                    const int from = s.len - key0;
+                    for (int j = L; j < (kTile - from) * 32; j += 128) {
+                        const int rr = from + (j >> 5), c = j & 31;
+                        *reinterpret_cast<uint4*>(sm.ring[st] + ((rr >> 5) * 4 + (c >> 3)) * kAtomBytes + (rr & 31) * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive0(&sm.p_full[bf]);
+            }
+            if (!alive) break;
+            // The next segment's queries first, so that its scores run during this one's epilogue.
+            const Seg cur = s;
+            ++seg;
+            have = next_seg(s);
+            if (have) take_q(r);
+            l += swap(l);                        // x + y = y + x: both halves hold the same sum
+            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag));
+            if (!alive) break;
+            tc::tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
+            const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
+            const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
+            const bool f32 = !whole || a.o_f32, write = grow < k.group_rows;
+            const size_t orow = (size_t)g * k.group_rows + grow, srow = (size_t)slot * kM + rank * kRows + row;
+            uint8_t* ws = static_cast<uint8_t*>(a.ws);
+            float* of = whole ? static_cast<float*>(a.o) + orow * kDv : reinterpret_cast<float*>(ws + kWsO) + srow * kDv;
+            uint16_t* ob = static_cast<uint16_t*>(a.o) + orow * kDv;
+            if (hf == 0 && write) {
+                if (!whole) reinterpret_cast<float*>(ws + kWsLse)[srow] = lse;
+                else if (a.lse) a.lse[orow] = lse;
+            }
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                uint32_t ov[32];
+                tc::tmem_ld32(tmem + c + lane_off, ov);
+                tc::tmem_wait_ld();
+                if (write) {
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                    if (f32) {
+                        float4* d = reinterpret_cast<float4*>(of + hf * 256 + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else {
+                        uint4* d = reinterpret_cast<uint4*>(ob + hf * 256 + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            d[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                              pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                    }
+                }
+                __syncwarp();
+            }
+            tc::tc_fence_before();               // the next segment's first product overwrites O after its p_full
+        }
+    } else if (busy && !FP8) {
+        // ---------------- BF16 loads.  Warp 6: queries and own keys; warp 7: the exchanged value rows
+        const bool xw = warp == 7;
+        const int R = k.box_rows, n_sub = kOwn / R;
+        const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;      // first key in a tile of the rows this warp loads
+        int r = 0, seg = 0;
+        uint32_t go_ph = 0;
+        bool ok = true;
+        Seg s;
+        while (ok && next_seg(s)) {
+            if (!xw) ok = load_q(s, r, seg++);
+            r += 2;
+            const int n = s.k1 - s.k0;
+            // Lane l holds the page and row of box l % n_sub of tile base + l / n_sub; 32 / n_sub tiles at a time.
+            const int batch = 32 / n_sub;
+            auto fetch = [&](int base, int* in_page) -> int {
+                const int key = (s.k0 + base + lane / n_sub) * kTile + my0 + (lane % n_sub) * R;
+                *in_page = 0;
+                if (base + lane / n_sub >= n || key >= s.len) return a.n_pages;   // outside the map: zeros
+                const int pg = page_of(s.seq, key, in_page);
+                // Sequences that share their rows (stride 0) are one in the map.
+                return pg < 0 ? a.n_pages : (a.table || a.seq_b ? pg : 0);
+            };
+            int nrow, npg = fetch(0, &nrow), crow = 0, cpg = 0;
+            for (int i = 0; i < n && ok; ++i, ++r) {
+                const int o = i % batch;
+                if (o == 0) {
+                    crow = nrow; cpg = npg;
+                    npg = fetch(i + batch, &nrow);
+                }
+                const int st = r % kStages;
+                if (xw) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    go_ph ^= 1u << st;
+                } else {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                }
+                if (!ok) break;
+                const uint32_t bar0 = tc::peer_smem(&sm.k_full[st], 0);
+                if (lane == 0) {
+                    if (xw) tc::mbar_expect_tx(&sm.x_full[st], kXBytes);
+                    else if (rank == 0) tc::mbar_expect_tx(&sm.k_full[st], 2 * kStageBytes);
+                }
+                __syncwarp();
+                const int n_at = xw ? 4 : kAtoms, at0 = xw ? rank * 4 : 0;         // atoms of the row to load
+                uint8_t* dst = sm.ring[st] + (xw ? (rank ^ 1) * kXBytes : 0);
+                const int n_box = n_sub == 1 ? 1 : n_sub * n_at;   // whole-tile boxes hold every atom
+                for (int b0 = 0; b0 < n_box; b0 += 32) {
+                    const int bx = b0 + lane, sub = bx % n_sub, at = bx / n_sub;
+                    const int pg = __shfl_sync(0xffffffffu, cpg, o * n_sub + sub), rw = __shfl_sync(0xffffffffu, crow, o * n_sub + sub);
+                    if (bx >= n_box) continue;
+                    uint8_t* d = dst + at * kAtomBytes + sub * R * 128;
+                    if (xw) tma_load_4d(d, &xmap, &sm.x_full[st], 0, rw, at0 + at, pg);
+                    else tma_load_4d_pair(d, &kmap, bar0, 0, rw, at0 + at, pg);
+                }
+            }
+        }
+    } else if (busy && FP8) {
+        // ---------------- FP8 loads: codes widened on the way.  Warps 6..11: own keys (and the queries); 12..15: exchanged rows
+        const bool xw = warp >= 6 + kKWarps;
+        const int w = xw ? warp - 6 - kKWarps : warp - 6;
+        const int tid = w * 32 + lane;
+        const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;
+        int r = 0, seg = 0;
+        uint32_t go_ph = 0;
+        bool ok = true;
+        Seg s;
+        while (ok && next_seg(s)) {
+            if (!xw && w == 0) ok = load_q(s, r, seg++);
+            r += 2;
+            const int n = s.k1 - s.k0;
+            constexpr int kPer = 6;              // 16-code chunks per thread: 32 x 36 / 192; exchanged rows 32 x 16 / 128 = 4
+            const int per_row = xw ? 16 : 36, stride = xw ? kXWarps * 32 : kKWarps * 32, cnt = xw ? 4 : kPer;
+            const int code0 = xw ? rank * 256 : 0;
+            // Lane l: offset of row l of tile i (own or exchanged), -1 behind the context.
+            auto row_at = [&](int i) -> int64_t {
+                const int key = (s.k0 + i) * kTile + my0 + lane;
+                if (i >= n || key >= s.len) return -1;
+                int rw;
+                const int pg = page_of(s.seq, key, &rw);
+                return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
+            };
+            // Lane l: scale of key 32 hh + l of tile i.
+            auto scale_at = [&](int i, int hh) -> float {
+                const int key = (s.k0 + i) * kTile + hh * 32 + lane;
+                if (i >= n || key >= s.len) return 0.f;
+                int rw;
+                const int pg = page_of(s.seq, key, &rw);
+                return pg < 0 ? 0.f : a.kv_scale[pg * a.scale_seq + rw];
+            };
+            auto load = [&](int64_t off, uint4 (&raw)[kPer]) {
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) {
+                    const int i = tid + c * stride, rr = i / per_row, q = i - rr * per_row;
+                    const int64_t ro = __shfl_sync(0xffffffffu, off, rr & 31);
+                    raw[c] = make_uint4(0, 0, 0, 0);
+                    if (c < cnt && ro >= 0) raw[c] = ldg_nc16(a.kv + ro + code0 + q * 16);
+                }
+            };
+            uint4 raw[kPer];
+            int64_t off1 = row_at(1);
+            load(row_at(0), raw);
+            float sc0 = 0.f, sc1 = 0.f;
+            if (!xw && w == 1) { sc0 = scale_at(0, 0); sc1 = scale_at(0, 1); }
+            for (int i = 0; i < n; ++i, ++r) {
+                uint4 cur[kPer];
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) cur[c] = raw[c];
+                const float c0 = sc0, c1 = sc1;
+                load(off1, raw);                 // the next tile's codes travel under this one
+                off1 = row_at(i + 2);
+                if (!xw && w == 1) { sc0 = scale_at(i + 1, 0); sc1 = scale_at(i + 1, 1); }
+                const int st = r % kStages;
+                if (xw) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    go_ph ^= 1u << st;
+                } else {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                }
+                if (!ok) break;
+                uint8_t* dst = sm.ring[st] + (xw ? (rank ^ 1) * kXBytes : 0);
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) {
+                    if (c >= cnt) continue;
+                    const int j = tid + c * stride, rr = j / per_row, q = j - rr * per_row;
+                    const uint2 w0 = widen4(cur[c].x), w1 = widen4(cur[c].y), w2 = widen4(cur[c].z), w3 = widen4(cur[c].w);
+                    uint8_t* d = dst + (q >> 2) * kAtomBytes + rr * 128;
+                    const int c8 = (q & 3) * 2;
+                    *reinterpret_cast<uint4*>(d + ((c8 ^ (rr & 7)) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                    *reinterpret_cast<uint4*>(d + (((c8 + 1) ^ (rr & 7)) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+                }
+                if (!xw && w == 1) {
+                    sm.kscale[st][lane] = c0;
+                    sm.kscale[st][32 + lane] = c1;
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (xw) tc::mbar_arrive(&sm.x_full[st]);
+                    else {
+                        if (w == 1) tc::mbar_arrive(&sm.sc_full[st]);
+                        arrive0(&sm.k_full[st]);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (*abort_flag) {                           // copies in flight land well within this time
+        const uint64_t t0 = tc::global_ns();
+        while (tc::global_ns() - t0 < 2000000ull) __nanosleep(1000);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync_all();                      // no CTA leaves while the other may still signal it
+    if (sm.abort && threadIdx.x == 0) report(a.status, LSA_ERR_TIMEOUT);
+    if (warp == 4) {
+        tc::tc_fence_after();
+        tmem_dealloc2(tmem, 512);
+    }
+}
+
+// Joins the partial results of the units that a run's start cuts.  Block (c, y): run c + 1's first unit, when that run
+// is the first to start inside it; warp = one of its rows.  Weights exp(lse - max), parts in key order.
+__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentKernelArgs k) {
+    const LatentArgs& a = k.a;
+    const WsHeader* w = static_cast<const WsHeader*>(a.ws);
+    const int c = blockIdx.x + 1, n_runs = w->clusters;
+    if (c >= n_runs || w->k0[c] == 0) return;
+    const int u = w->unit[c];
+    if (w->unit[c - 1] == u && w->k0[c - 1] > 0) return;           // an earlier run is the first
+    int last = c;
+    while (last + 1 < n_runs && w->unit[last + 1] == u) ++last;    // every later run of the unit starts inside it
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int g = u / k.m_tiles, grow = (u - g * k.m_tiles) * kM + row;
+    if (grow >= k.group_rows) return;
+    const float* lses = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kWsLse) + row;
+    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kWsO) + (size_t)row * kDv;
+    auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
+    const int n = last - c + 2;
+    float m = kNegInf;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, lses[slot(i) * kM]);
+    m = warp_max(m);
+    float acc[16], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    for (int i = 0; i < n; ++i) {
+        const float lse = lses[slot(i) * kM];
+        if (lse == kNegInf) continue;
+        const float wt = expf(lse - m);
+        sum += wt;
+        const float4* p = reinterpret_cast<const float4*>(parts + (size_t)slot(i) * kM * kDv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const size_t i = row * kDv + tid + e * kThreads;
-            if (a.o_f32) static_cast<float*>(a.o)[i] = acc[h][e] * inv;
-            else static_cast<__nv_bfloat16*>(a.o)[i] = __float2bfloat16_rn(acc[h][e] * inv);
+            const float4 v = p[e * 32 + lane];
+            acc[4 * e] = fmaf(wt, v.x, acc[4 * e]);
+            acc[4 * e + 1] = fmaf(wt, v.y, acc[4 * e + 1]);
+            acc[4 * e + 2] = fmaf(wt, v.z, acc[4 * e + 2]);
+            acc[4 * e + 3] = fmaf(wt, v.w, acc[4 * e + 3]);
         }
-        if (tid == 0 && a.lse) a.lse[row] = l > 0.f ? (s.m[h] + log2f(l)) * 0.69314718055994530942f : kNegInf;
     }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const size_t orow = (size_t)g * k.group_rows + grow;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float4 v = make_float4(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
+        if (a.o_f32) reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv)[e * 32 + lane] = v;
+        else reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + orow * kDv)[e * 32 + lane] =
+                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+    if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
+}
+
+// The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x `rows` x `chunks` x 1: `chunks` whole atoms in one load.
+bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int rows, int chunks) {
+    const bool one = a.n_pages == 1 || a.seq_b == 0;
+    const cuuint64_t d[4] = {64, (cuuint64_t)a.page_size, kAtoms, (cuuint64_t)(one ? 1 : a.n_pages)};
+    const cuuint64_t s[3] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)chunks, 1}, e[4] = {1, 1, 1, 1};
+    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(a.kv), d, s, box, e,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters that run at once on the current device (asked once per device).
+template <bool FP8>
+int cluster_count(size_t smem) {
+    static std::mutex mu;
+    static int known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (known[dev]) return known[dev];
+    if (cudaFuncSetAttribute(latent_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * kMaxClusters);
+    cfg.blockDim = dim3(kThreadsOf<FP8>);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {2, 1, 1};
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<FP8>, &cfg) != cudaSuccess || n < 1) return 0;
+    return known[dev] = n < kMaxClusters ? n : kMaxClusters;
+}
+
+template <bool FP8>
+cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& xm, LatentKernelArgs& k, cudaStream_t st) {
+    const size_t smem = sizeof(Smem) + 1024;
+    k.clusters = cluster_count<FP8>(smem);
+    if (k.clusters < 1) return cudaErrorInvalidConfiguration;
+    latent_attn_kernel<FP8><<<2 * k.clusters, kThreadsOf<FP8>, smem, st>>>(qm, km, xm, k);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || k.clusters == 1) return e;
+    latent_merge_kernel<<<dim3(k.clusters - 1, kM / 8), 256, 0, st>>>(k);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t latent_attn_ws(int, int, int) { return 256; }
+size_t latent_attn_ws(int, int, int) { return kWsBytes; }
 
 cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-    if (e != cudaSuccess) return e;
-    latent_attn_kernel<<<dim3(a.T, (a.H + kHeads - 1) / kHeads), kThreads, sizeof(Smem), st>>>(a);
-    return cudaGetLastError();
+    if (tc::encode_tiled() == nullptr) return cudaErrorNotSupported;
+    LatentKernelArgs k{};
+    k.a = a;
+    k.group_rows = a.q_group * a.H;
+    k.m_tiles = (k.group_rows + kM - 1) / kM;
+    k.units = a.T / a.q_group * k.m_tiles;
+    CUtensorMap qm, km, xm;
+    memset(&km, 0, sizeof(km));
+    memset(&xm, 0, sizeof(xm));
+    {
+        const cuuint64_t d[3] = {64, (cuuint64_t)a.T * a.H, kAtoms}, s[2] = {kD * 2, 128};
+        const cuuint32_t box[3] = {64, 32, kAtoms}, e[3] = {1, 1, 1};
+        if (tc::encode_tiled()(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), d, s, box, e,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
+    // Rows of a box: 32 keys at once where a page (or a sequence without pages, whose end may be inside a box) holds
+    // them whole, else 16 or 8, an atom at a time.
+    k.box_rows = !a.table || a.page_size % 32 == 0 ? 32 : (a.page_size % 16 == 0 ? 16 : 8);
+    const bool whole = k.box_rows == 32;
+    if (!make_kv_map(a, &km, k.box_rows, whole ? kAtoms : 1) || !make_kv_map(a, &xm, k.box_rows, whole ? 4 : 1)) return cudaErrorInvalidValue;
+    return launch_t<false>(qm, km, xm, k, st);
 }
 
 }  // namespace lsa

@@ -380,6 +380,20 @@ def test_latent_long_ragged_contexts(cuda, fp8):
     s.check()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,H,top", [(300, 128, 60), (400, 128, 200), (150, 300, 130), (250, 128, 700)])
+def test_latent_many_short_contexts(cuda, fp8, B, H, top):
+    """Many units per cluster, most of them of one to a few key tiles, padding among them."""
+    lens = [1 + (i * 7919) % top for i in range(B)]
+    pos = [[-1] if i % 13 == 5 else [n - 1] for i, n in enumerate(lens)]
+    s = Latent(B + top, H, lens, pos, page=16 if fp8 else 8 * (1 + B % 4), fp8=fp8)
+    s.run()
+    s.check()
+    o = s.o.clone()
+    s.run()
+    assert torch.equal(o, s.o)
+
+
 def test_latent_positions_inside_the_context(cuda):
     """Tokens in any order and not at the end; rows behind the group's last position are never used."""
     s = Latent(4, 48, [900, 400], [[700, 12, 0, 311, 699], [5, 4, 3, 2, 1]], page=40)
