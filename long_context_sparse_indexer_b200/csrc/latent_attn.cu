@@ -121,9 +121,23 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  :: "r"(tc::smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
-// Release-arrive on a barrier of CTA 0.
+// Arrive on a barrier of CTA 0.  What it signals stays on this SM (writes to its own shared memory, already
+// fenced for the tensor core that reads them, and tensor-memory accesses), so the release is at CTA scope: at
+// cluster scope it cost the warp 700 to 1,000 cycles, twice a tile.
 __device__ __forceinline__ void arrive0(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(tc::peer_smem(bar, 0)) : "memory");
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(tc::peer_smem(bar, 0)) : "memory");
+}
+// Waits on a barrier whose phase is at most a few hundred cycles away: polls without suspending.  Bounded.
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    for (int i = 0; i < 64; ++i)
+        if (tc::mbar_test_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::global_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (tc::mbar_test_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (tc::global_ns() - t0 > tc::kWaitNs) { *abort = 1; return false; }
+    }
 }
 // 4-D box into this CTA's shared memory, completing on the barrier at shared::cluster address bar of the pair's CTA 0.
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
@@ -377,11 +391,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 r += 2;                          // the queries' stages
                 const int n = s.k1 - s.k0;
                 if (leader) {
-                    ok = tc::mbar_wait_cluster(&sm.q_ready, seg & 1, abort_flag);
+                    ok = spin_wait(&sm.q_ready, seg & 1, abort_flag);
                     auto score = [&](int i) {
                         const int st = (r + i) % kStages, bf = (tile + i) & 1;
-                        ok = ok && tc::mbar_wait_cluster(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
-                             tc::mbar_wait_cluster(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
+                        ok = ok && spin_wait(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
+                             spin_wait(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
                         if (!ok) return;
                         k_ph ^= 1u << st;
                         tc::tc_fence_after();
@@ -403,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     for (int i = 0; i < n && ok; ++i) {
                         if (i + 2 < n) score(i + 2);
                         const int st = (r + i) % kStages, pb = (tile + i) & 1;
-                        ok = ok && tc::mbar_wait_cluster(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
+                        ok = ok && spin_wait(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
                         if (!ok) break;
                         tc::tc_fence_after();
                         const uint32_t va = tc::smem_u32(sm.ring[st]), pa = tc::smem_u32(sm.p[pb]);
@@ -428,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             if (leader && any) {                 // drain before TMEM is freed
                 volatile int drain = 0;
                 commit2(&sm.mma_done);
-                tc::mbar_wait_cluster(&sm.mma_done, 0, &drain);
+                spin_wait(&sm.mma_done, 0, &drain);
             }
         }
     } else if (busy && warp < 4) {
@@ -483,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             sm.mx[bf][L] = v;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.pair[warp & 1]);
-            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pair[warp & 1], swaps & 1, abort_flag));
+            alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pair[warp & 1], swaps & 1, abort_flag));
             ++swaps;
             return sm.mx[bf][L ^ 64];
         };
@@ -506,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     sc_ph ^= 1u << st;
                     if (!alive) break;
                 }
-                alive = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.s_full[bf], (tile >> 1) & 1, abort_flag));
+                alive = __all_sync(0xffffffffu, spin_wait(&sm.s_full[bf], (tile >> 1) & 1, abort_flag));
                 if (!alive) break;
                 tc::tc_fence_after();
                 uint32_t w[32];
@@ -552,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O must hold every product so far; P V of two tiles ago is known done, so the phase is unambiguous.
                     if (i > 0) {
-                        alive = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.pv_done[bf ^ 1], ((tile - 1) >> 1) & 1, abort_flag));
+                        alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[bf ^ 1], ((tile - 1) >> 1) & 1, abort_flag));
                         if (!alive) break;
                     }
                     tc::tc_fence_after();
@@ -587,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 // P into its buffer once the product two tiles ago has read it, and not before the tile's value rows are there.
-                if (tile >= 2) alive = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.pv_done[bf], ((tile >> 1) - 1) & 1, abort_flag));
+                if (tile >= 2) alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[bf], ((tile >> 1) - 1) & 1, abort_flag));
                 if (!alive) break;
                 uint8_t* prow = sm.p[bf] + row * 128;
 #pragma unroll
@@ -617,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             have = next_seg(s);
             if (have) take_q(r);
             l += swap(l);                        // x + y = y + x: both halves hold the same sum
-            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag));
+            alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag));
             if (!alive) break;
             tc::tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -690,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 const int st = r % kStages;
                 if (xw) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, spin_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
                     go_ph ^= 1u << st;
                 } else {
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
@@ -772,7 +786,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (!xw && w == 1) { sc0 = scale_at(i + 1, 0); sc1 = scale_at(i + 1, 1); }
                 const int st = r % kStages;
                 if (xw) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, spin_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
                     go_ph ^= 1u << st;
                 } else {
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
