@@ -27,7 +27,7 @@
 //
 // Warps: 0..3 softmax (thread = TMEM lane = (row, half of the keys); the two halves of a row exchange their
 // maxima through shared memory), 4 the MMAs (in CTA 0, for both), 5 the plan of the cluster's segments.  BF16:
-// 6 and 7 load keys and values by TMA, one box per tile for pages of whole 32 rows.  FP8: warps 6..11 and 12..15
+// 6 and 7 load keys and values by TMA.  FP8: warps 6..11 and 12..15
 // load codes and widen them to BF16 on the way to the same stages (bit moves and one exact multiply a pair).
 // All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
@@ -43,8 +43,12 @@ namespace {
 
 constexpr int kD = 576, kDv = 512, kM = 128, kRows = 64;         // unit rows, rows of a CTA
 constexpr int kTile = 64, kOwn = 32;                             // keys of a tile, of a CTA
-constexpr int kStages = 5, kAtoms = 9, kAtomBytes = kOwn * 128, kStageBytes = kAtoms * kAtomBytes;
-constexpr int kXBytes = 4 * kAtomBytes;
+constexpr int kStages = 5, kAtoms = 9, kStageBytes = kAtoms * kOwn * 128;
+// A stage's keys: groups of 8 rows, each nine 1 KB atoms of 8 rows x 64 dims.  Any run of 8 rows is one TMA box with
+// every dim, whatever the page size, and both operands' strides stay uniform (a group apart, an atom apart).
+constexpr int kAtom = 1024, kGroup = kAtoms * kAtom;
+constexpr int kQAtom = kOwn * 128;               // queries in a stage: 64-dim atoms of 32 rows
+constexpr int kXBytes = 4 * kOwn * 128;
 constexpr int kQTmem = 6;                                        // query atoms in TMEM, the others in shared memory
 constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
@@ -146,6 +150,11 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
         :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w, int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+        :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v) : "memory");
+}
 // 4-D box completing on a barrier of this CTA.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w) {
     asm volatile(
@@ -167,7 +176,8 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 struct LatentKernelArgs {
     LatentArgs a;
     int units, m_tiles, group_rows;              // units, units of a group, rows of a group
-    int clusters, box_rows;
+    int clusters;
+    int whole;                                   // a tile's 32 keys of a CTA are one TMA box (pages of whole 32 rows)
 };
 
 // Keys that some token of the unit sees (0: padding only), and its sequence.  `tell`: report bad tokens.
@@ -404,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         for (int at = 0; at < kAtoms; ++at)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                const uint64_t bd = tc::sdesc_sw128(ka + at * kAtomBytes + kk * 32);
+                                const uint64_t bd = tc::sdesc_sw128_lbo(ka + at * kAtom + kk * 32, 16, kGroup);
                                 if (at < kQTmem) mma2_ts(tmem + kSCol + bf * 32, tmem + kQCol + at * 32 + kk * 8, bd, idesc_s, (at | kk) != 0);
                                 else mma2_ss(tmem + kSCol + bf * 32, tc::sdesc_sw128(qa + (at - kQTmem) * (kRows * 128) + kk * 32), bd, idesc_s, 1u);
                             }
@@ -424,10 +434,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const uint64_t ad = tc::sdesc_sw128(pa + kk * 32);
-                            const uint32_t vk = va + (kk >> 1) * 4 * kAtomBytes + (kk & 1) * 2048;
+                            const uint32_t vk = va + (kk >> 1) * 4 * kAtom + (kk & 1) * 2 * kGroup;
 #pragma unroll
                             for (int ob = 0; ob < 2; ++ob)
-                                mma2_ss(tmem + ob * 128, ad, tc::sdesc_sw128_lbo(vk + ob * 2 * kAtomBytes, kAtomBytes, 1024), idesc_o,
+                                mma2_ss(tmem + ob * 128, ad, tc::sdesc_sw128_lbo(vk + ob * 2 * kAtom, kAtom, kGroup), idesc_o,
                                         (i | kk) != 0);
                         }
                         commit2(&sm.empty[st]);
@@ -463,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 uint32_t w[32];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + at * kAtomBytes + ((c ^ (row & 7)) << 4));
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + at * kQAtom + ((c ^ (row & 7)) << 4));
                     w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
                 }
                 tc::tmem_st32(tmem + kQCol + at * 32 + lane_off, w);
@@ -473,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)      // the same swizzle: bytes move as they are
                     *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + c) * 16) =
-                        *reinterpret_cast<const uint4*>(src + at * kAtomBytes + (4 * hf + c) * 16);
+                        *reinterpret_cast<const uint4*>(src + at * kQAtom + (4 * hf + c) * 16);
             tc::fence_proxy_async_smem();
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -615,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const int from = s.len - key0;
                     for (int j = L; j < (kTile - from) * 32; j += 128) {
                         const int rr = from + (j >> 5), c = j & 31;
-                        *reinterpret_cast<uint4*>(sm.ring[st] + ((rr >> 5) * 4 + (c >> 3)) * kAtomBytes + (rr & 31) * 128 + (c & 7) * 16) =
+                        *reinterpret_cast<uint4*>(sm.ring[st] + ((rr & 31) >> 3) * kGroup + ((rr >> 5) * 4 + (c >> 3)) * kAtom + (rr & 7) * 128 + (c & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
                 }
@@ -675,7 +685,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     } else if (busy && !FP8) {
         // ---------------- BF16 loads.  Warp 6: queries and own keys; warp 7: the exchanged value rows
         const bool xw = warp == 7;
-        const int R = k.box_rows, n_sub = kOwn / R;
         const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;      // first key in a tile of the rows this warp loads
         int r = 0, seg = 0;
         uint32_t go_ph = 0;
@@ -685,22 +694,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             if (!xw) ok = load_q(s, r, seg++);
             r += 2;
             const int n = s.k1 - s.k0;
-            // Lane l holds the page and row of box l % n_sub of tile base + l / n_sub; 32 / n_sub tiles at a time.
-            const int batch = 32 / n_sub;
+            // Lane l: page and first row of 8-row group l % 4 of tile base + l / 4; 8 tiles at a time.
             auto fetch = [&](int base, int* in_page) -> int {
-                const int key = (s.k0 + base + lane / n_sub) * kTile + my0 + (lane % n_sub) * R;
+                const int key = (s.k0 + base + lane / 4) * kTile + my0 + (lane % 4) * 8;
                 *in_page = 0;
-                if (base + lane / n_sub >= n || key >= s.len) return a.n_pages;   // outside the map: zeros
+                if (base + lane / 4 >= n || key >= s.len) return a.n_pages;        // outside the map: zeros
                 const int pg = page_of(s.seq, key, in_page);
                 // Sequences that share their rows (stride 0) are one in the map.
                 return pg < 0 ? a.n_pages : (a.table || a.seq_b ? pg : 0);
             };
             int nrow, npg = fetch(0, &nrow), crow = 0, cpg = 0;
             for (int i = 0; i < n && ok; ++i, ++r) {
-                const int o = i % batch;
+                const int o = i % 8;
                 if (o == 0) {
                     crow = nrow; cpg = npg;
-                    npg = fetch(i + batch, &nrow);
+                    npg = fetch(i + 8, &nrow);
                 }
                 const int st = r % kStages;
                 if (xw) {
@@ -716,16 +724,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     else if (rank == 0) tc::mbar_expect_tx(&sm.k_full[st], 2 * kStageBytes);
                 }
                 __syncwarp();
-                const int n_at = xw ? 4 : kAtoms, at0 = xw ? rank * 4 : 0;         // atoms of the row to load
-                uint8_t* dst = sm.ring[st] + (xw ? (rank ^ 1) * kXBytes : 0);
-                const int n_box = n_sub == 1 ? 1 : n_sub * n_at;   // whole-tile boxes hold every atom
-                for (int b0 = 0; b0 < n_box; b0 += 32) {
-                    const int bx = b0 + lane, sub = bx % n_sub, at = bx / n_sub;
-                    const int pg = __shfl_sync(0xffffffffu, cpg, o * n_sub + sub), rw = __shfl_sync(0xffffffffu, crow, o * n_sub + sub);
-                    if (bx >= n_box) continue;
-                    uint8_t* d = dst + at * kAtomBytes + sub * R * 128;
-                    if (xw) tma_load_4d(d, &xmap, &sm.x_full[st], 0, rw, at0 + at, pg);
-                    else tma_load_4d_pair(d, &kmap, bar0, 0, rw, at0 + at, pg);
+                const int pg = __shfl_sync(0xffffffffu, cpg, o * 4 + (lane & 3)), rw = __shfl_sync(0xffffffffu, crow, o * 4 + (lane & 3));
+                if (xw) {                        // 256 dims of 8 rows a box
+                    if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + (rank ^ 1) * 4 * kAtom, &xmap, &sm.x_full[st], 0, rw, rank * 4, pg);
+                } else if (k.whole) {            // 32 rows in one box
+                    if (lane == 0) tma_load_5d_pair(sm.ring[st], &kmap, bar0, 0, 0, 0, rw / 8, pg);
+                } else if (lane < 4) {           // 8 rows a box
+                    tma_load_4d_pair(sm.ring[st] + lane * kGroup, &kmap, bar0, 0, rw, 0, pg);
                 }
             }
         }
@@ -792,13 +797,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                 }
                 if (!ok) break;
-                uint8_t* dst = sm.ring[st] + (xw ? (rank ^ 1) * kXBytes : 0);
+                uint8_t* dst = sm.ring[st] + (xw ? (rank ^ 1) * 4 * kAtom : 0);
 #pragma unroll
                 for (int c = 0; c < kPer; ++c) {
                     if (c >= cnt) continue;
                     const int j = tid + c * stride, rr = j / per_row, q = j - rr * per_row;
                     const uint2 w0 = widen4(cur[c].x), w1 = widen4(cur[c].y), w2 = widen4(cur[c].z), w3 = widen4(cur[c].w);
-                    uint8_t* d = dst + (q >> 2) * kAtomBytes + rr * 128;
+                    uint8_t* d = dst + (rr >> 3) * kGroup + (q >> 2) * kAtom + (rr & 7) * 128;
                     const int c8 = (q & 3) * 2;
                     *reinterpret_cast<uint4*>(d + ((c8 ^ (rr & 7)) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
                     *reinterpret_cast<uint4*>(d + (((c8 + 1) ^ (rr & 7)) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
@@ -885,13 +890,24 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant
     if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
 }
 
-// The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x `rows` x `chunks` x 1: `chunks` whole atoms in one load.
-bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int rows, int chunks) {
+// The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x 8 x `chunks` x 1.
+bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int chunks) {
     const bool one = a.n_pages == 1 || a.seq_b == 0;
     const cuuint64_t d[4] = {64, (cuuint64_t)a.page_size, kAtoms, (cuuint64_t)(one ? 1 : a.n_pages)};
     const cuuint64_t s[3] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)chunks, 1}, e[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)chunks, 1}, e[4] = {1, 1, 1, 1};
     return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(a.kv), d, s, box, e,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// (64 dims, 8 rows, 9 chunks, groups of 8 rows, pages), box 64 x 8 x 9 x 4 x 1: a CTA's keys of a tile, in a stage's order.
+bool make_tile_map(const LatentArgs& a, CUtensorMap* m) {
+    const bool one = a.n_pages == 1 || a.seq_b == 0;
+    const cuuint64_t d[5] = {64, 8, kAtoms, (cuuint64_t)(a.page_size / 8), (cuuint64_t)(one ? 1 : a.n_pages)};
+    const cuuint64_t s[4] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)a.tok_b * 8, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
+    const cuuint32_t box[5] = {64, 8, kAtoms, 4, 1}, e[5] = {1, 1, 1, 1, 1};
+    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(a.kv), d, s, box, e,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -955,11 +971,10 @@ cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
             return cudaErrorInvalidValue;
     }
     if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
-    // Rows of a box: 32 keys at once where a page (or a sequence without pages, whose end may be inside a box) holds
-    // them whole, else 16 or 8, an atom at a time.
-    k.box_rows = !a.table || a.page_size % 32 == 0 ? 32 : (a.page_size % 16 == 0 ? 16 : 8);
-    const bool whole = k.box_rows == 32;
-    if (!make_kv_map(a, &km, k.box_rows, whole ? kAtoms : 1) || !make_kv_map(a, &xm, k.box_rows, whole ? 4 : 1)) return cudaErrorInvalidValue;
+    // One box per CTA and tile where pages hold 32 rows whole; a sequence without pages may end inside 8 rows, which
+    // only the map by single rows bounds.
+    k.whole = a.page_size % 32 == 0;
+    if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, kAtoms)) || !make_kv_map(a, &xm, 4)) return cudaErrorInvalidValue;
     return launch_t<false>(qm, km, xm, k, st);
 }
 
