@@ -25,10 +25,10 @@
 // 64-dim atoms of 32 keys, atoms 0..3 / 4..7 doubling as the value rows of keys 0..31 / 32..63.  Queries arrive
 // through two stages of the same ring.
 //
-// Warps: 0..3 softmax (thread = TMEM lane = (row, half of the keys); the two halves of a row exchange their
-// maxima through shared memory), 4 the MMAs (in CTA 0, for both), 5 the plan of the cluster's segments.  BF16:
-// 6 and 7 load keys and values by TMA.  FP8: warps 6..11 and 12..15
-// load codes and widen them to BF16 on the way to the same stages (bit moves and one exact multiply a pair).
+// Warps: 0..3 and 4..7 softmax, alternate tiles (thread = TMEM lane = (row, half of the keys); the two halves of a row
+// exchange their maxima through shared memory), 8 the MMAs (in CTA 0, for both), 9 the plan of the cluster's segments.
+// BF16: 10 and 11 load keys and values by TMA.  FP8: 10..15 and 16..19 load codes and widen them to BF16 on the way to
+// the same stages (bit moves and one exact multiply a pair).
 // All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
 #include <cstring>
@@ -53,6 +53,7 @@ constexpr int kQTmem = 6;                                        // query atoms 
 constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
 constexpr int kMaxClusters = 80;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kPlanWarp = 9, kLoadWarp = 10;   // from kLoadWarp on: loads
 constexpr int kKWarps = 6, kXWarps = 4;                          // FP8 converters
 static_assert(kQCol + kQTmem * 32 == 512, "TMEM columns");
 
@@ -65,7 +66,13 @@ struct Smem {
     alignas(1024) uint8_t q[kAtoms - kQTmem][kRows * 128];
     alignas(1024) uint8_t p[2][kRows * 128];
     float kscale[kStages][kTile];                // FP8: the tile's row scales
-    float mx[2][128];                            // what the halves of a row exchange: tile maxima, sums
+    float mx[2][2][128];                         // what the halves of a row exchange, per warpgroup: tile maxima, sums
+    float m_ref[128];                            // the reference maximum after the latest decided tile
+    float m_last[2][kRows];                      // each warpgroup's last reference, and its sums by half
+    union {
+        float l_last[2][128];
+        long long scan[32];                      // the plan's warp sums, before any tile
+    };
     Seg seg[kSegs];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t k_full[kStages];                    // CTA 0: both CTAs' keys have landed
@@ -75,11 +82,12 @@ struct Smem {
     uint64_t q_full, q_ready;                    // queries staged; (CTA 0) moved to their operand places in both CTAs
     uint64_t s_full[2], s_free[2];               // scores done; (CTA 0) read by both CTAs
     uint64_t p_full[2], pv_done[2];              // (CTA 0) weights and value rows in place; their product done
-    uint64_t pair[2];                            // softmax warps w and w + 2: the halves' values are written
+    uint64_t pair[2][2];                         // softmax warps w and w + 2 of a warpgroup: the halves' values are written
+    uint64_t hand[2][4];                         // warpgroup w, quarter q: m_ref of its tile is out
+    uint64_t both;                               // every softmax warp has written its last reference and sum
+    uint64_t o_read;                             // every softmax warp has read O
     uint64_t q_taken;                            // every softmax warp has read the staged queries
     uint64_t mma_done;
-    long long scan[32];
-    long long total;
     int u0, k0;                                  // where the cluster's run starts
     uint32_t tmem_base;
     int abort;
@@ -204,7 +212,7 @@ __device__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
 }
 
 template <bool FP8>
-constexpr int kThreadsOf = FP8 ? 32 * (6 + kKWarps + kXWarps) : 32 * 8;
+constexpr int kThreadsOf = 32 * (kLoadWarp + (FP8 ? kKWarps + kXWarps : 2));
 
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
@@ -222,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         constexpr int kLoaders = FP8 ? kKWarps + kXWarps : 2;
         for (int i = 0; i < kSegs; ++i) {
             tc::mbar_init(&sm.seg_full[i], 1);
-            tc::mbar_init(&sm.seg_empty[i], 4 + kLoaders + (rank == 0 ? 1 : 0));
+            tc::mbar_init(&sm.seg_empty[i], kSoftmaxWarps + kLoaders + (rank == 0 ? 1 : 0));
         }
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sm.k_full[i], FP8 ? 2 * kKWarps : 1);
@@ -232,20 +240,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             tc::mbar_init(&sm.empty[i], 1);
         }
         tc::mbar_init(&sm.q_full, 1);
-        tc::mbar_init(&sm.q_ready, 8);
-        tc::mbar_init(&sm.q_taken, 4);
+        tc::mbar_init(&sm.q_ready, 2 * kSoftmaxWarps);
+        tc::mbar_init(&sm.q_taken, kSoftmaxWarps);
+        tc::mbar_init(&sm.o_read, kSoftmaxWarps);
+        tc::mbar_init(&sm.both, kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sm.s_full[i], 1);
             tc::mbar_init(&sm.s_free[i], 8);
             tc::mbar_init(&sm.p_full[i], 8);
             tc::mbar_init(&sm.pv_done[i], 1);
-            tc::mbar_init(&sm.pair[i], 2);
+            for (int j = 0; j < 2; ++j) tc::mbar_init(&sm.pair[i][j], 2);
+            for (int j = 0; j < 4; ++j) tc::mbar_init(&sm.hand[i][j], 1);
         }
         tc::mbar_init(&sm.mma_done, 1);
         sm.abort = 0;
         tc::fence_barrier_init();
     }
-    if (warp == 4) tmem_alloc2(&sm.tmem_base, 512);
+    if (warp == kMmaWarp) tmem_alloc2(&sm.tmem_base, 512);
 
     // The plan: tiles per unit, summed over the block; each thread takes a run of units.
     const int per = (k.units + kThreads - 1) / kThreads;
@@ -297,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     tc::tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    // Segments, as every role but warp 5 takes them.
+    // Segments, as every role but the plan takes them.
     int seg_i = 0;
     auto next_seg = [&](Seg& s) -> bool {
         const int d = seg_i % kSegs;
@@ -334,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         return ok;
     };
 
-    if (warp == 5) {
+    if (warp == kPlanWarp) {
         // ---------------- plan: the run's segments, then the units that hold padding only
         if (busy) {
             int seg = 0, u = sm.u0, k0 = sm.k0;
@@ -388,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     for (int i = lane; i < n; i += 32) a.lse[row + i] = kNegInf;
             }
         }
-    } else if (busy && warp == 4) {
+    } else if (busy && warp == kMmaWarp) {
         // ---------------- MMA issuer (CTA 0)
         if (rank == 0) {
             const uint32_t idesc_s = tc::idesc_f16(128, kTile, 1), idesc_o = tc::idesc_f16_bmn(128, 256, 1);
@@ -455,21 +466,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 spin_wait(&sm.mma_done, 0, &drain);
             }
         }
-    } else if (busy && warp < 4) {
-        // ---------------- softmax: lane L of TMEM = row L & 63, keys 32 (L >> 6) .. + 31 of a tile
-        const int L = warp * 32 + lane, row = L & 63, hf = L >> 6;
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        int r = 0, tile = 0, seg = 0;
-        uint32_t x_ph = 0, sc_ph = 0;
+    } else if (busy && warp < kSoftmaxWarps) {
+        // ---------------- softmax: lane L of TMEM = row L & 63, keys 32 (L >> 6) .. + 31 of a tile.  Warpgroup wg takes
+        // the tiles of score buffer and P buffer wg
+        const int wg = warp >> 2, quarter = warp & 3, L = quarter * 32 + lane, row = L & 63, hf = L >> 6;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        int r = 0, tile = 0, seg = 0;            // ring position and key tiles before the segment, segments so far
+        uint32_t stage_ph = 0, hand_ph = 0;      // parity of each stage's next phase; of the next hand-over
         bool alive = true;
         Seg s;
-        // Queries of the next segment from the two stages at ring position r to their operand places.
+        // Queries of the next segment from the two stages at ring position r to their operand places; each warpgroup
+        // takes half the atoms.
         auto take_q = [&](int r) {
             alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_full, seg & 1, abort_flag));
             if (!alive) return;
             const uint8_t* src = sm.ring[(r + (row >> 5)) % kStages] + (row & 31) * 128;
-#pragma unroll 2
-            for (int at = 0; at < kQTmem; ++at) {
+#pragma unroll
+            for (int a3 = 0; a3 < kQTmem / 2; ++a3) {
+                const int at = wg * (kQTmem / 2) + a3;
                 uint32_t w[32];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -478,12 +492,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 tc::tmem_st32(tmem + kQCol + at * 32 + lane_off, w);
             }
+            // The other atoms keep their swizzle: bytes move as they are, a quarter of a row per thread.
 #pragma unroll
             for (int at = kQTmem; at < kAtoms; ++at)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)      // the same swizzle: bytes move as they are
-                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + c) * 16) =
-                        *reinterpret_cast<const uint4*>(src + at * kQAtom + (4 * hf + c) * 16);
+                for (int c = 0; c < 2; ++c)
+                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + 2 * wg + c) * 16) =
+                        *reinterpret_cast<const uint4*>(src + at * kQAtom + (4 * hf + 2 * wg + c) * 16);
             tc::fence_proxy_async_smem();
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -500,16 +515,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
             }
         };
-        // The value of the other half of this row (its thread is in warp w ^ 2).
+        // The value of the other half of this row (its thread is two warps away in the warpgroup).
         int swaps = 0;
         auto swap = [&](float v) -> float {
             const int bf = swaps & 1;
-            sm.mx[bf][L] = v;
+            sm.mx[wg][bf][L] = v;
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.pair[warp & 1]);
-            alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pair[warp & 1], swaps & 1, abort_flag));
+            if (lane == 0) tc::mbar_arrive(&sm.pair[wg][quarter & 1]);
+            alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pair[wg][quarter & 1], swaps & 1, abort_flag));
             ++swaps;
-            return sm.mx[bf][L ^ 64];
+            return sm.mx[wg][bf][L ^ 64];
         };
         bool have = next_seg(s);
         if (have) take_q(0);
@@ -522,23 +537,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 const int t = g * a.q_group + grow / a.H, pos = a.q_pos[t];
                 if (pos >= 0 && a.q_seq[t] == s.seq && pos < a.seq_len[s.seq]) lim = pos + 1;
             }
-            float m = kNegInf, l = 0.f;
-            for (int i = 0; i < n; ++i, ++r, ++tile) {
-                const int bf = tile & 1, st = r % kStages, key0 = (s.k0 + i) * kTile;
-                if (FP8) {
-                    alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sc_full[st], (sc_ph >> st) & 1, abort_flag));
-                    sc_ph ^= 1u << st;
-                    if (!alive) break;
-                }
-                alive = __all_sync(0xffffffffu, spin_wait(&sm.s_full[bf], (tile >> 1) & 1, abort_flag));
+            float m = kNegInf, l = 0.f;          // reference maximum this warpgroup last used, its sum
+            for (int i = (tile ^ wg) & 1; i < n; i += 2) {
+                const int tl = tile + i, st = (r + i) % kStages, key0 = (s.k0 + i) * kTile;
+                alive = __all_sync(0xffffffffu, spin_wait(&sm.s_full[wg], (tl >> 1) & 1, abort_flag));
                 if (!alive) break;
                 tc::tc_fence_after();
+                // A stage comes round every kStages tiles; its phases before this tile's are complete, since the tile's keys
+                // replaced a stage whose product was done.
+                const uint32_t turn = (stage_ph >> st ^ i / kStages) & 1;
+                if (FP8) {
+                    alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sc_full[st], turn, abort_flag));
+                    if (!alive) break;
+                }
                 uint32_t w[32];
-                tc::tmem_ld32(tmem + kSCol + bf * 32 + lane_off, w);
+                tc::tmem_ld32(tmem + kSCol + wg * 32 + lane_off, w);
                 tc::tmem_wait_ld();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive0(&sm.s_free[bf]);
+                if (lane == 0) arrive0(&sm.s_free[wg]);
                 float x[32];
                 if constexpr (FP8) {
                     const float4* ks = reinterpret_cast<const float4*>(&sm.kscale[st][hf * 32]);
@@ -560,36 +577,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     for (int e = 0; e < 32; ++e)
                         if (e >= left) x[e] = kNegInf;
                 }
-                float mt = x[0];
+                float mx[8];
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mt = fmaxf(mt, x[e]);
+                for (int e = 0; e < 8; ++e) mx[e] = fmaxf(fmaxf(x[e], x[e + 8]), fmaxf(x[e + 16], x[e + 24]));
+                float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                 mt = fmaxf(mt, swap(mt));
-                if (!alive) break;
-                // The reference rises only when the tile exceeds it by more than 2^8 (both halves alike).
-                float alpha = 1.f;
-                bool rescale = false;
-                if (mt > m + 8.f) {
-                    if (m != kNegInf) { alpha = ex2(m - mt); rescale = true; }
-                    l *= alpha;
-                    m = mt;
+                // The reference rises only when the tile exceeds it by more than 2^8 (both halves alike).  These decisions are
+                // one chain over the segment's tiles, handed from one warpgroup to the other.
+                float m_prev = m;
+                if (i > 0) {
+                    alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.hand[wg ^ 1][quarter], hand_ph, abort_flag));
+                    hand_ph ^= 1;
+                    m_prev = sm.m_ref[L];
                 }
-                if (__any_sync(0xffffffffu, rescale)) {
-                    // O must hold every product so far; P V of two tiles ago is known done, so the phase is unambiguous.
-                    if (i > 0) {
-                        alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[bf ^ 1], ((tile - 1) >> 1) & 1, abort_flag));
-                        if (!alive) break;
-                    }
-                    tc::tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        uint32_t ov[32];
-                        tc::tmem_ld32(tmem + c + lane_off, ov);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        tc::tmem_st32(tmem + c + lane_off, ov);
-                    }
-                    tc::tmem_wait_st();
+                if (!alive) break;
+                float alpha = 1.f, m_new = m_prev;
+                bool rescale = false;
+                if (mt > m_prev + 8.f) {
+                    if (m_prev != kNegInf) { alpha = ex2(m_prev - mt); rescale = true; }
+                    m_new = mt;
+                }
+                if (i + 1 < n) {
+                    sm.m_ref[L] = m_new;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sm.hand[wg][quarter]);
+                }
+                if (m_new != m) {                // this warpgroup's sum to the new reference
+                    l = m == kNegInf ? 0.f : l * ex2(m - m_new);
+                    m = m_new;
                 }
                 const float mref = m == kNegInf ? 0.f : m;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -610,16 +625,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     pw[e / 2 + 1] = pack_bf16x2(p2, p3);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                // P into its buffer once the product two tiles ago has read it, and not before the tile's value rows are there.
-                if (tile >= 2) alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[bf], ((tile >> 1) - 1) & 1, abort_flag));
+                // P into its buffer once the product two tiles ago has read it.
+                if (tl >= 2) alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[wg], ((tl >> 1) - 1) & 1, abort_flag));
                 if (!alive) break;
-                uint8_t* prow = sm.p[bf] + row * 128;
+                uint8_t* prow = sm.p[wg] + row * 128;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<uint4*>(prow + (((4 * hf + c) ^ (row & 7)) << 4)) =
                         make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
-                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_full[st], (x_ph >> st) & 1, abort_flag));
-                x_ph ^= 1u << st;
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O must hold every product before this tile's: P V of the tile before, whose barrier's earlier phase
+                    // (three tiles ago) is complete -- this tile's scores were issued after that product.
+                    if (i > 0) {
+                        alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[wg ^ 1], ((tl - 1) >> 1) & 1, abort_flag));
+                        if (!alive) break;
+                    }
+                    tc::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 32) {
+                        uint32_t ov[32];
+                        tc::tmem_ld32(tmem + c + lane_off, ov);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tc::tmem_st32(tmem + c + lane_off, ov);
+                    }
+                    tc::tmem_wait_st();
+                }
+                // Not before the tile's value rows are there.
+                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_full[st], turn, abort_flag));
                 if (!alive) break;
                 if (!FP8 && key0 + kTile > s.len) {                // value rows behind the last key: zero
                     const int from = s.len - key0;
@@ -632,16 +666,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 tc::fence_proxy_async_smem();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive0(&sm.p_full[bf]);
+                if (lane == 0) arrive0(&sm.p_full[wg]);
             }
+            // The stages' parities move on for the tiles of both warpgroups.
+            if (n / kStages & 1) stage_ph ^= (1u << kStages) - 1;
+            for (int i = n - n % kStages; i < n; ++i) stage_ph ^= 1u << ((r + i) % kStages);
+            r += n;
+            tile += n;
             if (!alive) break;
             // The next segment's queries first, so that its scores run during this one's epilogue.
             const Seg cur = s;
             ++seg;
             have = next_seg(s);
-            if (have) take_q(r);
+            // Both warpgroups' sums at the larger of their references; past this barrier both have seen their last scores,
+            // so the queries may be replaced.
+            if (hf == 0) sm.m_last[wg][row] = m;
+            sm.l_last[wg][L] = l;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.both);
+            alive = __all_sync(0xffffffffu, spin_wait(&sm.both, (seg - 1) & 1, abort_flag));
+            if (!alive) break;
+            const float m0 = sm.m_last[0][row], m1 = sm.m_last[1][row];
+            m = fmaxf(m0, m1);
+            l = (m0 == kNegInf ? 0.f : sm.l_last[0][L] * ex2(m0 - m)) + (m1 == kNegInf ? 0.f : sm.l_last[1][L] * ex2(m1 - m));
             l += swap(l);                        // x + y = y + x: both halves hold the same sum
-            alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag));
+            if (have) take_q(r);
+            for (int j = max(0, tile - 2); j < tile; ++j)          // both buffers' last products
+                alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
             if (!alive) break;
             tc::tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -653,12 +704,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             uint8_t* ws = static_cast<uint8_t*>(a.ws);
             float* of = whole ? static_cast<float*>(a.o) + orow * kDv : reinterpret_cast<float*>(ws + kWsO) + srow * kDv;
             uint16_t* ob = static_cast<uint16_t*>(a.o) + orow * kDv;
-            if (hf == 0 && write) {
+            if (hf == 0 && wg == 0 && write) {
                 if (!whole) reinterpret_cast<float*>(ws + kWsLse)[srow] = lse;
                 else if (a.lse) a.lse[orow] = lse;
             }
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = wg * 128; c < wg * 128 + 128; c += 32) {
                 uint32_t ov[32];
                 tc::tmem_ld32(tmem + c + lane_off, ov);
                 tc::tmem_wait_ld();
@@ -680,11 +731,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 __syncwarp();
             }
-            tc::tc_fence_before();               // the next segment's first product overwrites O after its p_full
+            // The next segment's first product overwrites O: not before both warpgroups have read theirs.
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.o_read);
+            if (have) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_read, (seg - 1) & 1, abort_flag));
         }
     } else if (busy && !FP8) {
-        // ---------------- BF16 loads.  Warp 6: queries and own keys; warp 7: the exchanged value rows
-        const bool xw = warp == 7;
+        // ---------------- BF16 loads.  First warp: queries and own keys; second: the exchanged value rows
+        const bool xw = warp == kLoadWarp + 1;
         const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;      // first key in a tile of the rows this warp loads
         int r = 0, seg = 0;
         uint32_t go_ph = 0;
@@ -735,9 +790,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         }
     } else if (busy && FP8) {
-        // ---------------- FP8 loads: codes widened on the way.  Warps 6..11: own keys (and the queries); 12..15: exchanged rows
-        const bool xw = warp >= 6 + kKWarps;
-        const int w = xw ? warp - 6 - kKWarps : warp - 6;
+        // ---------------- FP8 loads: codes widened on the way.  First six warps: own keys (and the queries); four: exchanged rows
+        const bool xw = warp >= kLoadWarp + kKWarps;
+        const int w = xw ? warp - kLoadWarp - kKWarps : warp - kLoadWarp;
         const int tid = w * 32 + lane;
         const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;
         int r = 0, seg = 0;
@@ -833,7 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     __syncthreads();
     tc::cluster_sync_all();                      // no CTA leaves while the other may still signal it
     if (sm.abort && threadIdx.x == 0) report(a.status, LSA_ERR_TIMEOUT);
-    if (warp == 4) {
+    if (warp == kMmaWarp) {
         tc::tc_fence_after();
         tmem_dealloc2(tmem, 512);
     }
