@@ -139,18 +139,6 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
 __device__ __forceinline__ void arrive0(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(tc::peer_smem(bar, 0)) : "memory");
 }
-// Waits on a barrier whose phase is at most a few hundred cycles away: polls without suspending.  Bounded.
-__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    for (int i = 0; i < 64; ++i)
-        if (tc::mbar_test_wait(bar, parity)) return true;
-    const uint64_t t0 = tc::global_ns();
-    for (;;) {
-        for (int i = 0; i < 64; ++i)
-            if (tc::mbar_test_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (tc::global_ns() - t0 > tc::kWaitNs) { *abort = 1; return false; }
-    }
-}
 // 4-D box into this CTA's shared memory, completing on the barrier at shared::cluster address bar of the pair's CTA 0.
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
     asm volatile(
@@ -412,11 +400,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 r += 2;                          // the queries' stages
                 const int n = s.k1 - s.k0;
                 if (leader) {
-                    ok = spin_wait(&sm.q_ready, seg & 1, abort_flag);
+                    ok = tc::mbar_wait(&sm.q_ready, seg & 1, abort_flag);
                     auto score = [&](int i) {
                         const int st = (r + i) % kStages, bf = (tile + i) & 1;
-                        ok = ok && spin_wait(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
-                             spin_wait(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
+                        ok = ok && tc::mbar_wait(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
+                             tc::mbar_wait(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
                         if (!ok) return;
                         k_ph ^= 1u << st;
                         tc::tc_fence_after();
@@ -433,13 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         commit2(&sm.x_go[st]);
                         any = true;
                     };
-                    if (ok) score(0);
-                    if (ok && n > 1) score(1);
-                    for (int i = 0; i < n && ok; ++i) {
-                        if (i + 2 < n) score(i + 2);
+                    auto weigh = [&](int i) {
                         const int st = (r + i) % kStages, pb = (tile + i) & 1;
-                        ok = ok && spin_wait(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
-                        if (!ok) break;
+                        ok = ok && tc::mbar_wait(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
+                        if (!ok) return;
                         tc::tc_fence_after();
                         const uint32_t va = tc::smem_u32(sm.ring[st]), pa = tc::smem_u32(sm.p[pb]);
 #pragma unroll
@@ -453,6 +438,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         }
                         commit2(&sm.empty[st]);
                         commit2(&sm.pv_done[pb]);
+                    };
+                    // S runs two tiles ahead of P V.
+                    if (ok) score(0);
+                    if (ok && n > 1) score(1);
+                    for (int i = 0; i < n && ok; ++i) {
+                        if (i + 2 < n) score(i + 2);
+                        if (ok) weigh(i);
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
@@ -463,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             if (leader && any) {                 // drain before TMEM is freed
                 volatile int drain = 0;
                 commit2(&sm.mma_done);
-                spin_wait(&sm.mma_done, 0, &drain);
+                tc::mbar_wait(&sm.mma_done, 0, &drain);
             }
         }
     } else if (busy && warp < kSoftmaxWarps) {
@@ -522,7 +514,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             sm.mx[wg][bf][L] = v;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.pair[wg][quarter & 1]);
-            alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pair[wg][quarter & 1], swaps & 1, abort_flag));
+            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pair[wg][quarter & 1], swaps & 1, abort_flag));
             ++swaps;
             return sm.mx[wg][bf][L ^ 64];
         };
@@ -540,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             float m = kNegInf, l = 0.f;          // reference maximum this warpgroup last used, its sum
             for (int i = (tile ^ wg) & 1; i < n; i += 2) {
                 const int tl = tile + i, st = (r + i) % kStages, key0 = (s.k0 + i) * kTile;
-                alive = __all_sync(0xffffffffu, spin_wait(&sm.s_full[wg], (tl >> 1) & 1, abort_flag));
+                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[wg], (tl >> 1) & 1, abort_flag));
                 if (!alive) break;
                 tc::tc_fence_after();
                 // A stage comes round every kStages tiles; its phases before this tile's are complete, since the tile's keys
@@ -556,7 +548,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive0(&sm.s_free[wg]);
+                // Scores in log2 units: x = w * sc for BF16 (sc folded into the exponent's multiply-add), w for FP8 after the
+                // rows' scales.
                 float x[32];
+                const float sc = FP8 ? 1.f : a.sm_scale_log2;
                 if constexpr (FP8) {
                     const float4* ks = reinterpret_cast<const float4*>(&sm.kscale[st][hf * 32]);
 #pragma unroll
@@ -569,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(w[e]) * a.sm_scale_log2;
+                    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(w[e]);
                 }
                 const int left = lim - key0 - hf * 32;
                 if (__any_sync(0xffffffffu, left < 32)) {
@@ -580,13 +575,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 float mx[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mx[e] = fmaxf(fmaxf(x[e], x[e + 8]), fmaxf(x[e + 16], x[e + 24]));
-                float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc;
                 mt = fmaxf(mt, swap(mt));
                 // The reference rises only when the tile exceeds it by more than 2^8 (both halves alike).  These decisions are
                 // one chain over the segment's tiles, handed from one warpgroup to the other.
                 float m_prev = m;
                 if (i > 0) {
-                    alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.hand[wg ^ 1][quarter], hand_ph, abort_flag));
+                    alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.hand[wg ^ 1][quarter], hand_ph, abort_flag));
                     hand_ph ^= 1;
                     m_prev = sm.m_ref[L];
                 }
@@ -607,26 +602,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     m = m_new;
                 }
                 const float mref = m == kNegInf ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-mref, -mref);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t pw[16];
-                const float4* vs = reinterpret_cast<const float4*>(&sm.kscale[st][hf * 32]);
+                const float2* vs = reinterpret_cast<const float2*>(&sm.kscale[st][hf * 32]);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float p0 = ex2(x[e] - mref), p1 = ex2(x[e + 1] - mref), p2 = ex2(x[e + 2] - mref), p3 = ex2(x[e + 3] - mref);
-                    sum[0] += p0; sum[1] += p1; sum[2] += p2; sum[3] += p3;
+                for (int e = 0; e < 16; ++e) {
+                    float2 p = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, m2);
+                    p.x = ex2(p.x);
+                    p.y = ex2(p.y);
+                    sum[e & 1].x += p.x;
+                    sum[e & 1].y += p.y;
                     if constexpr (FP8) {                           // the row's scale goes into its weight (a masked row's may be anything)
-                        const float4 v = vs[e / 4];
-                        p0 = p0 > 0.f ? p0 * v.x : 0.f;
-                        p1 = p1 > 0.f ? p1 * v.y : 0.f;
-                        p2 = p2 > 0.f ? p2 * v.z : 0.f;
-                        p3 = p3 > 0.f ? p3 * v.w : 0.f;
+                        const float2 v = vs[e];
+                        p.x = p.x > 0.f ? p.x * v.x : 0.f;
+                        p.y = p.y > 0.f ? p.y * v.y : 0.f;
                     }
-                    pw[e / 2] = pack_bf16x2(p0, p1);
-                    pw[e / 2 + 1] = pack_bf16x2(p2, p3);
+                    pw[e] = pack_bf16x2(p.x, p.y);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 // P into its buffer once the product two tiles ago has read it.
-                if (tl >= 2) alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[wg], ((tl >> 1) - 1) & 1, abort_flag));
+                if (tl >= 2) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[wg], ((tl >> 1) - 1) & 1, abort_flag));
                 if (!alive) break;
                 uint8_t* prow = sm.p[wg] + row * 128;
 #pragma unroll
@@ -637,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     // O must hold every product before this tile's: P V of the tile before, whose barrier's earlier phase
                     // (three tiles ago) is complete -- this tile's scores were issued after that product.
                     if (i > 0) {
-                        alive = __all_sync(0xffffffffu, spin_wait(&sm.pv_done[wg ^ 1], ((tl - 1) >> 1) & 1, abort_flag));
+                        alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[wg ^ 1], ((tl - 1) >> 1) & 1, abort_flag));
                         if (!alive) break;
                     }
                     tc::tc_fence_after();
@@ -684,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             sm.l_last[wg][L] = l;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.both);
-            alive = __all_sync(0xffffffffu, spin_wait(&sm.both, (seg - 1) & 1, abort_flag));
+            alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.both, (seg - 1) & 1, abort_flag));
             if (!alive) break;
             const float m0 = sm.m_last[0][row], m1 = sm.m_last[1][row];
             m = fmaxf(m0, m1);
@@ -692,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             l += swap(l);                        // x + y = y + x: both halves hold the same sum
             if (have) take_q(r);
             for (int j = max(0, tile - 2); j < tile; ++j)          // both buffers' last products
-                alive = alive && __all_sync(0xffffffffu, spin_wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
+                alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
             if (!alive) break;
             tc::tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -767,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 const int st = r % kStages;
                 if (xw) {
-                    ok = __all_sync(0xffffffffu, spin_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
                     go_ph ^= 1u << st;
                 } else {
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
@@ -846,7 +842,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (!xw && w == 1) { sc0 = scale_at(i + 1, 0); sc1 = scale_at(i + 1, 1); }
                 const int st = r % kStages;
                 if (xw) {
-                    ok = __all_sync(0xffffffffu, spin_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
                     go_ph ^= 1u << st;
                 } else {
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
