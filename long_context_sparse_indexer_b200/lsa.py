@@ -371,36 +371,41 @@ def kvp_local_index(batch: Batch, shard_start: torch.Tensor, shard_len: torch.Te
                                     _ptr(local_count), _ptr(dev_status), _stream(stream)), "lsa_kvp_local_index")
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor on the current CUDA device, where the call is launched."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _launch_device(*tensors) -> int:
+    """The device of the tensors (None: absent): one CUDA device, the current one, where the call is launched."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"tensor on {t.device}: the call runs on the current device (cuda:{dev})")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {tensors[0].device}: the call runs on the current CUDA device")
+    return dev
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The handle of `stream`, or of the device's current stream (torch.cuda.current_stream without its checks)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _float_vec(t: Optional[torch.Tensor], n: int, name: str) -> None:
-    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n):
+    if t is not None and (t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous()):
         raise ValueError(f"{name}: a contiguous float32 tensor of {n} elements")
 
 
 def _int_vec(t: torch.Tensor, n: int, name: str) -> None:
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements")
 
 
-def _check_batch_vecs(b: Batch) -> None:
-    _int_vec(b.q_seq, b.q_seq.numel(), "q_seq")
-    _int_vec(b.q_pos, b.q_seq.numel(), "q_pos")
-    _int_vec(b.seq_len, b.seq_len.numel(), "seq_len")
-
-
-def _check_cache(c: Cache) -> None:
-    if c.data.dim() != 3 or c.data.stride(2) != 1:
-        raise ValueError("cache: [sequences or pages, rows, dim] with contiguous rows")
-    if c.dtype == FP8_E4M3 and (c.scale is None or c.scale.dtype != torch.float32 or c.scale.dim() != 2
-                                or c.scale.stride(1) != 1 or c.scale.shape != c.data.shape[:2]):
-        raise ValueError("cache scale: float32 [sequences or pages, rows] with contiguous rows")
+def _batch_c(b: Batch, T: int) -> CBatch:
+    """The C batch of checked vectors."""
+    _int_vec(b.q_seq, T, "q_seq")
+    _int_vec(b.q_pos, T, "q_pos")
+    B = b.seq_len.numel()
+    _int_vec(b.seq_len, B, "seq_len")
+    return CBatch(B, T, b.q_group, b.L_alloc, b.seq_len.data_ptr(), b.q_seq.data_ptr(), b.q_pos.data_ptr())
 
 
 class Rope:
@@ -433,22 +438,33 @@ class PageTable:
 
     def c(self, cache: Cache) -> CPages:
         t = self.table
-        if t.dim() != 2 or t.dtype != torch.int32 or t.stride(1) != 1:
+        if t.dim() != 2 or t.dtype is not torch.int32 or t.stride(1) != 1:
             raise ValueError("page table: int32 [sequences, pages per sequence] with contiguous rows")
-        return CPages(_ptr(t), int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1]), int(t.shape[1]),
-                      int(cache.data.shape[1]), int(cache.data.shape[0]), 0)
+        B, n = t.shape
+        return CPages(t.data_ptr(), t.stride(0) if B > 1 else n, n, cache.data.shape[1], cache.data.shape[0], 0)
 
 
-def _pages(pages: Optional[PageTable], cache: Cache, batch: Batch):
-    """The C page table of a checked cache, or None; a cache without pages holds the batch's sequences."""
-    _check_cache(cache)
+def _cache_c(cache: Cache, pages: Optional[PageTable], B: int, rows: int):
+    """The C cache and page table (None: a cache of the batch's B sequences of at least `rows` rows), checked."""
+    d, sc = cache.data, cache.scale
+    if d.dim() != 3 or d.stride(2) != 1:
+        raise ValueError("cache: [sequences or pages, rows, dim] with contiguous rows")
+    n, r, dim = d.shape
+    dt = cache.dtype
+    sss = 0
+    if dt == FP8_E4M3:
+        if sc is None or sc.dtype is not torch.float32 or sc.shape != d.shape[:2] or sc.stride(1) != 1:
+            raise ValueError("cache scale: float32 [sequences or pages, rows] with contiguous rows")
+        sss = sc.stride(0)
+    cc = CCache(d.data_ptr(), sc.data_ptr() if sss else None, dt, dim, d.stride(0), d.stride(1), sss)
     if pages is None:
-        if cache.data.shape[0] < batch.seq_len.numel() or cache.data.shape[1] < batch.L_alloc:
+        if n < B or r < rows:
             raise ValueError("cache: fewer sequences or rows than the batch")
-        return None
-    if pages.table.shape[0] < batch.seq_len.numel():
+        return cc, None
+    cp = pages.c(cache)
+    if pages.table.shape[0] < B:
         raise ValueError("page table: fewer sequences than the batch")
-    return ctypes.byref(pages.c(cache))
+    return cc, cp
 
 
 def rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: Optional[torch.Tensor] = None, offset: int = 0,
@@ -457,19 +473,27 @@ def rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: Optional[torch.Tenso
     contiguous dimensions) rotated by pos [T] int32 into y, in place when y is None.  backward: the rotation by
     the negative angle, which takes the gradient of y to that of x.  Returns y."""
     y = x if y is None else y
-    if x.dim() != 3 or y.shape != x.shape or y.dtype != x.dtype or x.dtype not in (torch.bfloat16, torch.float32):
+    dt = x.dtype
+    if x.dim() != 3 or y.shape != x.shape or y.dtype is not dt or (dt is not torch.bfloat16 and dt is not torch.float32):
         raise ValueError("rope: x and y are [T, H, D] of one type, bf16 or float32")
-    if x.shape[2] > 1 and (x.stride(2) != 1 or y.stride(2) != 1):
+    T, H, D = x.shape
+    (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
+    if D > 1 and (xd != 1 or yd != 1):
         raise ValueError("rope: the last dimension is contiguous")
-    T, H, D = (int(n) for n in x.shape)
     _int_vec(pos, T, "pos")
-    _same_device(pos, x, y)
+    dev = _launch_device(x, y, pos)
     # A dimension of one element has no stride that matters (and may report zero for an expanded one).
-    st = lambda t, i: int(t.stride(i)) if t.shape[i] > 1 else D  # noqa: E731
-    _check(_lib.lsa_rope_apply(ctypes.byref(rope.c), T, H, D, int(offset), _ptr(pos),
-                               BF16 if x.dtype == torch.bfloat16 else FP32, _ptr(x), st(x, 0), st(x, 1), _ptr(y),
-                               st(y, 0), st(y, 1), int(bool(backward)), _stream(stream)), "lsa_rope_apply")
+    if T == 1:
+        xt = yt = D
+    if H == 1:
+        xh = yh = D
+    _check(_lib.lsa_rope_apply(rope.c, T, H, D, offset, pos.data_ptr(), BF16 if dt is torch.bfloat16 else FP32,
+                               x.data_ptr(), xt, xh, y.data_ptr(), yt, yh, 1 if backward else 0, _stream_on(dev, stream)),
+           "lsa_rope_apply")
     return y
+
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
 def cache_append(batch: Batch, x: torch.Tensor, cache: Cache, pages: Optional[PageTable] = None, norm: str = "none",
@@ -478,24 +502,21 @@ def cache_append(batch: Batch, x: torch.Tensor, cache: Cache, pages: Optional[Pa
                  dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """lsa_cache_append: the rows x [T, dim] (bf16), normalised ("none", "rms" or "layer" over the first norm_dim
     elements, default all), rotated (rope, at rope_offset) and stored at each token's position of the cache."""
-    kinds = {"none": 0, "rms": 1, "layer": 2}
-    if norm not in kinds:
+    if norm not in _NORMS:
         raise ValueError(f"unknown norm {norm!r}")
-    T, dim = int(batch.q_seq.numel()), int(cache.data.shape[2])
-    if x.dim() != 2 or x.shape[0] != T or x.shape[1] != dim or x.dtype != torch.bfloat16 or x.stride(1) != 1:
+    T, dim = batch.q_seq.numel(), cache.data.shape[-1]
+    if x.dim() != 2 or x.shape != (T, dim) or x.dtype is not torch.bfloat16 or x.stride(1) != 1:
         raise ValueError("cache_append: x is [T, dim] bf16 with contiguous rows")
     norm_dim = int(norm_dim or dim)
     _float_vec(gamma, norm_dim, "gamma")
     _float_vec(beta, norm_dim, "beta")
-    _check_batch_vecs(batch)
-    cp = _pages(pages, cache, batch)
-    _same_device(x, cache.data, cache.scale, gamma, beta, dev_status, batch.q_pos, batch.q_seq, batch.seq_len,
-                 pages.table if pages else None)
-    cb, cc = batch.c(), cache.c()
-    _check(_lib.lsa_cache_append(ctypes.byref(cb), _ptr(x), int(x.stride(0)) if T > 1 else dim, kinds[norm], norm_dim,
-                                 _ptr(gamma), _ptr(beta), float(eps), ctypes.byref(rope.c) if rope else None,
-                                 int(rope_offset), ctypes.byref(cc), cp, _ptr(dev_status), _stream(stream)),
-           "lsa_cache_append")
+    cb = _batch_c(batch, T)
+    cc, cp = _cache_c(cache, pages, cb.B, batch.L_alloc)
+    dev = _launch_device(x, cache.data, cache.scale, gamma, beta, dev_status, batch.q_pos, batch.q_seq, batch.seq_len,
+                         None if pages is None else pages.table)
+    _check(_lib.lsa_cache_append(cb, x.data_ptr(), x.stride(0) if T > 1 else dim, _NORMS[norm], norm_dim, _ptr(gamma),
+                                 _ptr(beta), eps, None if rope is None else rope.c, rope_offset, cc, cp,
+                                 _ptr(dev_status), _stream_on(dev, stream)), "lsa_cache_append")
 
 
 def latent_attn_workspace_size(T: int, q_group: int, H: int) -> int:
@@ -503,9 +524,10 @@ def latent_attn_workspace_size(T: int, q_group: int, H: int) -> int:
 
 
 def _out_dtype(o: torch.Tensor, shape) -> int:
-    if tuple(o.shape) != tuple(shape) or not o.is_contiguous() or o.dtype not in (torch.bfloat16, torch.float32):
+    dt = o.dtype
+    if o.shape != shape or not o.is_contiguous() or (dt is not torch.bfloat16 and dt is not torch.float32):
         raise ValueError(f"o: contiguous bf16 or float32 {list(shape)}")
-    return BF16 if o.dtype == torch.bfloat16 else FP32
+    return BF16 if dt is torch.bfloat16 else FP32
 
 
 def latent_attn(batch: Batch, q: torch.Tensor, cache: Cache, sm_scale: float, o: torch.Tensor,
@@ -513,20 +535,19 @@ def latent_attn(batch: Batch, q: torch.Tensor, cache: Cache, sm_scale: float, o:
                 dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """lsa_latent_attn: q [T, H, 576] bf16 over every cached row up to each token's position -> o [T, H, 512]
     (bf16, or float32 for a later merge_partials), lse [T, H] float32.  ws: latent_attn_workspace_size bytes."""
-    T = int(batch.q_seq.numel())
-    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != 576 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    T = batch.q_seq.numel()
+    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != 576 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
         raise ValueError("latent_attn: q is contiguous bf16 [T, H, 576]")
-    H = int(q.shape[1])
+    H = q.shape[1]
     dt = _out_dtype(o, (T, H, 512))
     _float_vec(lse, T * H, "lse")
-    _check_batch_vecs(batch)
-    cp = _pages(pages, cache, batch)
-    _same_device(q, o, lse, ws, dev_status, cache.data, cache.scale, batch.q_pos, batch.q_seq, batch.seq_len,
-                 pages.table if pages else None)
-    cb, cc = batch.c(), cache.c()
-    _check(_lib.lsa_latent_attn(ctypes.byref(cb), _ptr(q), H, ctypes.byref(cc), cp, float(sm_scale), _ptr(o), dt,
-                                _ptr(lse), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
-                                _ptr(dev_status), _stream(stream)), "lsa_latent_attn")
+    cb = _batch_c(batch, T)
+    cc, cp = _cache_c(cache, pages, cb.B, batch.L_alloc)
+    dev = _launch_device(q, o, lse, ws, dev_status, cache.data, cache.scale, batch.q_pos, batch.q_seq, batch.seq_len,
+                         None if pages is None else pages.table)
+    _check(_lib.lsa_latent_attn(cb, q.data_ptr(), H, cc, cp, sm_scale, o.data_ptr(), dt, _ptr(lse), _ptr(ws),
+                                0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status),
+                                _stream_on(dev, stream)), "lsa_latent_attn")
 
 
 def latent_attn_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
@@ -536,24 +557,33 @@ def latent_attn_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Te
     """lsa_latent_attn_expanded: packed sequences, q [T, H, 192], k_nope and v [S, H, 128] and the shared k_rope
     [S, 64] (bf16, contiguous last dimension) -> o [T, H, 128] (bf16 or float32), lse [T, H] float32.  q_start /
     k_start [B + 1] int32: the sequences' rows; max_q: the longest sequence's query count."""
-    if (q.dim() != 3 or q.shape[2] != 192 or k_nope.dim() != 3 or k_nope.shape[1:] != (q.shape[1], 128)
-            or v.shape != k_nope.shape or k_rope.shape != (k_nope.shape[0], 64)):
+    if q.dim() != 3 or k_nope.dim() != 3:
         raise ValueError("latent_attn_expanded: q [T, H, 192], k_nope and v [S, H, 128], k_rope [S, 64]")
-    if any(t.dtype != torch.bfloat16 or t.stride(-1) != 1 for t in (q, k_nope, k_rope, v)):
+    T, H, dq = q.shape
+    S = k_nope.shape[0]
+    if dq != 192 or k_nope.shape != (S, H, 128) or v.shape != (S, H, 128) or k_rope.shape != (S, 64):
+        raise ValueError("latent_attn_expanded: q [T, H, 192], k_nope and v [S, H, 128], k_rope [S, 64]")
+    (qt, qh, qd), (kt, kh, kd), (rt, rd), (vt, vh, vd) = q.stride(), k_nope.stride(), k_rope.stride(), v.stride()
+    bf = torch.bfloat16
+    if q.dtype is not bf or k_nope.dtype is not bf or k_rope.dtype is not bf or v.dtype is not bf or not qd == kd == rd == vd == 1:
         raise ValueError("latent_attn_expanded: bf16 inputs with a contiguous last dimension")
-    T, H, S = int(q.shape[0]), int(q.shape[1]), int(k_nope.shape[0])
     dt = _out_dtype(o, (T, H, 128))
     _float_vec(lse, T * H, "lse")
-    B = int(q_start.numel()) - 1
+    B = q_start.numel() - 1
     _int_vec(q_start, B + 1, "q_start")
     _int_vec(k_start, B + 1, "k_start")
-    _same_device(q, k_nope, k_rope, v, q_start, k_start, o, lse, dev_status)
+    dev = _launch_device(q, k_nope, k_rope, v, q_start, k_start, o, lse, dev_status)
     # A dimension of one element has no stride that matters.
-    st = lambda t, i: int(t.stride(i)) if t.shape[i] > 1 else 0  # noqa: E731
-    _check(_lib.lsa_latent_attn_expanded(B, T, S, H, int(max_q), _ptr(q_start), _ptr(k_start), _ptr(q), st(q, 0), st(q, 1),
-                                         _ptr(k_nope), st(k_nope, 0), st(k_nope, 1), _ptr(k_rope), st(k_rope, 0),
-                                         _ptr(v), st(v, 0), st(v, 1), float(sm_scale), int(bool(causal)), _ptr(o), dt,
-                                         _ptr(lse), _ptr(dev_status), _stream(stream)), "lsa_latent_attn_expanded")
+    if T == 1:
+        qt = 0
+    if H == 1:
+        qh = kh = vh = 0
+    if S == 1:
+        kt = rt = vt = 0
+    _check(_lib.lsa_latent_attn_expanded(B, T, S, H, max_q, q_start.data_ptr(), k_start.data_ptr(), q.data_ptr(), qt, qh,
+                                         k_nope.data_ptr(), kt, kh, k_rope.data_ptr(), rt, v.data_ptr(), vt, vh, sm_scale,
+                                         1 if causal else 0, o.data_ptr(), dt, _ptr(lse), _ptr(dev_status),
+                                         _stream_on(dev, stream)), "lsa_latent_attn_expanded")
 
 
 @dataclass
