@@ -27,8 +27,8 @@
 //
 // Warps: 0..3 and 4..7 softmax, alternate tiles (thread = TMEM lane = (row, half of the keys); the two halves of a row
 // exchange their maxima through shared memory), 8 the MMAs (in CTA 0, for both), 9 the plan of the cluster's segments.
-// BF16: 10 and 11 load keys and values by TMA.  FP8: 10..15 and 16..19 load codes and widen them to BF16 on the way to
-// the same stages (bit moves and one exact multiply a pair).
+// BF16: 10 and 11 load keys and exchanged rows by TMA.  FP8: 10 loads a tile's codes into the head of the stage that
+// they widen into, 11..16 widen them there and 17..20 the exchanged rows (bit moves and one exact multiply a pair).
 // All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
 #include <cstring>
@@ -49,6 +49,8 @@ constexpr int kStages = 5, kAtoms = 9, kStageBytes = kAtoms * kOwn * 128;
 constexpr int kAtom = 1024, kGroup = kAtoms * kAtom;
 constexpr int kQAtom = kOwn * 128;               // queries in a stage: 64-dim atoms of 32 rows
 constexpr int kXBytes = 4 * kOwn * 128;
+// FP8: a CTA's codes of a tile land at the head of the stage they widen into, as 8-row groups of three 192-dim runs.
+constexpr int kCodeRun = 192, kCodeGroup = 8 * kD, kCodeBytes = kOwn * kD;
 constexpr int kQTmem = 6;                                        // query atoms in TMEM, the others in shared memory
 constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
@@ -77,6 +79,8 @@ struct Smem {
     uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t k_full[kStages];                    // CTA 0: both CTAs' keys have landed
     uint64_t sc_full[kStages];                   // FP8: kscale is written
+    uint64_t code_full[kStages];                 // FP8: the stage's codes have landed
+    uint64_t code_read;                          // FP8: every converter of own keys holds its codes in registers
     uint64_t x_go[kStages], x_full[kStages];     // the scores of the stage are done; its exchanged rows have landed
     uint64_t empty[kStages];
     uint64_t q_full, q_ready;                    // queries staged; (CTA 0) moved to their operand places in both CTAs
@@ -151,7 +155,12 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m
         "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
         :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v) : "memory");
 }
-// 4-D box completing on a barrier of this CTA.
+// Boxes completing on a barrier of this CTA.
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w, int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+        :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v) : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
@@ -200,7 +209,7 @@ __device__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
 }
 
 template <bool FP8>
-constexpr int kThreadsOf = 32 * (kLoadWarp + (FP8 ? kKWarps + kXWarps : 2));
+constexpr int kThreadsOf = 32 * (kLoadWarp + (FP8 ? 1 + kKWarps + kXWarps : 2));
 
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
@@ -215,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     volatile int* abort_flag = &sm.abort;
 
     if (threadIdx.x == 0) {
-        constexpr int kLoaders = FP8 ? kKWarps + kXWarps : 2;
+        constexpr int kLoaders = FP8 ? 1 + kKWarps + kXWarps : 2;
         for (int i = 0; i < kSegs; ++i) {
             tc::mbar_init(&sm.seg_full[i], 1);
             tc::mbar_init(&sm.seg_empty[i], kSoftmaxWarps + kLoaders + (rank == 0 ? 1 : 0));
@@ -223,11 +232,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sm.k_full[i], FP8 ? 2 * kKWarps : 1);
             tc::mbar_init(&sm.sc_full[i], 1);
+            tc::mbar_init(&sm.code_full[i], 1);
             tc::mbar_init(&sm.x_go[i], 1);
             tc::mbar_init(&sm.x_full[i], FP8 ? kXWarps : 1);
             tc::mbar_init(&sm.empty[i], 1);
         }
         tc::mbar_init(&sm.q_full, 1);
+        tc::mbar_init(&sm.code_read, kKWarps);
         tc::mbar_init(&sm.q_ready, 2 * kSoftmaxWarps);
         tc::mbar_init(&sm.q_taken, kSoftmaxWarps);
         tc::mbar_init(&sm.o_read, kSoftmaxWarps);
@@ -733,9 +744,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             if (lane == 0) tc::mbar_arrive(&sm.o_read);
             if (have) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_read, (seg - 1) & 1, abort_flag));
         }
-    } else if (busy && !FP8) {
-        // ---------------- BF16 loads.  First warp: queries and own keys; second: the exchanged value rows
-        const bool xw = warp == kLoadWarp + 1;
+    } else if (busy && warp < kLoadWarp + (FP8 ? 1 : 2)) {
+        // ---------------- TMA loads.  First warp: queries and own keys (FP8: their codes); second: the exchanged value rows
+        const bool xw = !FP8 && warp == kLoadWarp + 1;
         const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;      // first key in a tile of the rows this warp loads
         int r = 0, seg = 0;
         uint32_t go_ph = 0;
@@ -772,12 +783,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 const uint32_t bar0 = tc::peer_smem(&sm.k_full[st], 0);
                 if (lane == 0) {
                     if (xw) tc::mbar_expect_tx(&sm.x_full[st], kXBytes);
+                    else if (FP8) tc::mbar_expect_tx(&sm.code_full[st], kCodeBytes);
                     else if (rank == 0) tc::mbar_expect_tx(&sm.k_full[st], 2 * kStageBytes);
                 }
                 __syncwarp();
                 const int pg = __shfl_sync(0xffffffffu, cpg, o * 4 + (lane & 3)), rw = __shfl_sync(0xffffffffu, crow, o * 4 + (lane & 3));
                 if (xw) {                        // 256 dims of 8 rows a box
                     if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + (rank ^ 1) * 4 * kAtom, &xmap, &sm.x_full[st], 0, rw, rank * 4, pg);
+                } else if (FP8) {
+                    if (k.whole) {
+                        if (lane == 0) tma_load_5d(sm.ring[st], &kmap, &sm.code_full[st], 0, 0, 0, rw / 8, pg);
+                    } else if (lane < 4) {
+                        tma_load_4d(sm.ring[st] + lane * kCodeGroup, &kmap, &sm.code_full[st], 0, rw, 0, pg);
+                    }
                 } else if (k.whole) {            // 32 rows in one box
                     if (lane == 0) tma_load_5d_pair(sm.ring[st], &kmap, bar0, 0, 0, 0, rw / 8, pg);
                 } else if (lane < 4) {           // 8 rows a box
@@ -786,91 +804,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         }
     } else if (busy && FP8) {
-        // ---------------- FP8 loads: codes widened on the way.  First six warps: own keys (and the queries); four: exchanged rows
-        const bool xw = warp >= kLoadWarp + kKWarps;
-        const int w = xw ? warp - kLoadWarp - kKWarps : warp - kLoadWarp;
-        const int tid = w * 32 + lane;
-        const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;
-        int r = 0, seg = 0;
-        uint32_t go_ph = 0;
+        // ---------------- FP8: codes to BF16.  First six warps: own keys, from the codes landed in the stage; four: the
+        // exchanged rows, from global memory (the other CTA has brought them into L2)
+        const bool xw = warp > kLoadWarp + kKWarps;
+        const int w = xw ? warp - kLoadWarp - kKWarps - 1 : warp - kLoadWarp - 1, tid = w * 32 + lane;
+        int r = 0, tile = 0;
+        uint32_t ph = 0;                         // parity of each stage's next phase (codes landed; scores done)
         bool ok = true;
         Seg s;
-        while (ok && next_seg(s)) {
-            if (!xw && w == 0) ok = load_q(s, r, seg++);
-            r += 2;
-            const int n = s.k1 - s.k0;
-            constexpr int kPer = 6;              // 16-code chunks per thread: 32 x 36 / 192; exchanged rows 32 x 16 / 128 = 4
-            const int per_row = xw ? 16 : 36, stride = xw ? kXWarps * 32 : kKWarps * 32, cnt = xw ? 4 : kPer;
-            const int code0 = xw ? rank * 256 : 0;
-            // Lane l: offset of row l of tile i (own or exchanged), -1 behind the context.
-            auto row_at = [&](int i) -> int64_t {
-                const int key = (s.k0 + i) * kTile + my0 + lane;
-                if (i >= n || key >= s.len) return -1;
-                int rw;
-                const int pg = page_of(s.seq, key, &rw);
-                return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
-            };
-            // Lane l: scale of key 32 hh + l of tile i.
-            auto scale_at = [&](int i, int hh) -> float {
-                const int key = (s.k0 + i) * kTile + hh * 32 + lane;
-                if (i >= n || key >= s.len) return 0.f;
-                int rw;
-                const int pg = page_of(s.seq, key, &rw);
-                return pg < 0 ? 0.f : a.kv_scale[pg * a.scale_seq + rw];
-            };
-            auto load = [&](int64_t off, uint4 (&raw)[kPer]) {
+        auto put = [&](uint8_t* d, uint4 v) {    // 16 codes: two 16-byte chunks next to each other under the swizzle
+            const uint2 w0 = widen4(v.x), w1 = widen4(v.y), w2 = widen4(v.z), w3 = widen4(v.w);
+            *reinterpret_cast<uint4*>(d) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>((uintptr_t)d ^ 16)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+        };
+        // Place in a stage of 16 dims (chunk q of the row's 36) of row rr.
+        auto place = [&](int rr, int q) { return (rr >> 3) * kGroup + (q >> 2) * kAtom + (rr & 7) * 128 + ((((q & 3) * 2) ^ (rr & 7)) << 4); };
+        if (!xw) {
+            constexpr int kPer = 6;              // 16-code chunks per thread: 32 x 36 / 192
+            int dst[kPer];
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) {
-                    const int i = tid + c * stride, rr = i / per_row, q = i - rr * per_row;
-                    const int64_t ro = __shfl_sync(0xffffffffu, off, rr & 31);
-                    raw[c] = make_uint4(0, 0, 0, 0);
-                    if (c < cnt && ro >= 0) raw[c] = ldg_nc16(a.kv + ro + code0 + q * 16);
+            for (int c = 0; c < kPer; ++c) {
+                const int i = tid + c * kKWarps * 32, g = i / 288, part = i % 288 / 96, r8 = i % 96 / 12;
+                dst[c] = place(g * 8 + r8, part * 12 + i % 12);
+            }
+            while (ok && next_seg(s)) {
+                r += 2;
+                const int n = s.k1 - s.k0;
+                // Row scales (second warp; lane l: keys l and l + 32): found two tiles ahead, loaded one ahead.
+                auto scale_at = [&](int i, int hh) -> const float* {
+                    const int key = (s.k0 + i) * kTile + hh * 32 + lane;
+                    if (i >= n || key >= s.len) return nullptr;
+                    int rw;
+                    const int pg = page_of(s.seq, key, &rw);
+                    return pg < 0 ? nullptr : a.kv_scale + pg * a.scale_seq + rw;
+                };
+                const float *at0 = nullptr, *at1 = nullptr;
+                float sc0 = 0.f, sc1 = 0.f;
+                if (w == 1) {
+                    at0 = scale_at(0, 0); at1 = scale_at(0, 1);
+                    if (at0) sc0 = __ldg(at0);
+                    if (at1) sc1 = __ldg(at1);
+                    at0 = scale_at(1, 0); at1 = scale_at(1, 1);
                 }
-            };
-            uint4 raw[kPer];
-            int64_t off1 = row_at(1);
-            load(row_at(0), raw);
-            float sc0 = 0.f, sc1 = 0.f;
-            if (!xw && w == 1) { sc0 = scale_at(0, 0); sc1 = scale_at(0, 1); }
-            for (int i = 0; i < n; ++i, ++r) {
-                uint4 cur[kPer];
+                for (int i = 0; i < n; ++i, ++r, ++tile) {
+                    const int st = r % kStages;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_full[st], (ph >> st) & 1, abort_flag));
+                    ph ^= 1u << st;
+                    if (!ok) break;
+                    uint4 raw[kPer];
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) cur[c] = raw[c];
-                const float c0 = sc0, c1 = sc1;
-                load(off1, raw);                 // the next tile's codes travel under this one
-                off1 = row_at(i + 2);
-                if (!xw && w == 1) { sc0 = scale_at(i + 1, 0); sc1 = scale_at(i + 1, 1); }
-                const int st = r % kStages;
-                if (xw) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
-                    go_ph ^= 1u << st;
-                } else {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
-                }
-                if (!ok) break;
-                uint8_t* dst = sm.ring[st] + (xw ? (rank ^ 1) * 4 * kAtom : 0);
-#pragma unroll
-                for (int c = 0; c < kPer; ++c) {
-                    if (c >= cnt) continue;
-                    const int j = tid + c * stride, rr = j / per_row, q = j - rr * per_row;
-                    const uint2 w0 = widen4(cur[c].x), w1 = widen4(cur[c].y), w2 = widen4(cur[c].z), w3 = widen4(cur[c].w);
-                    uint8_t* d = dst + (rr >> 3) * kGroup + (q >> 2) * kAtom + (rr & 7) * 128;
-                    const int c8 = (q & 3) * 2;
-                    *reinterpret_cast<uint4*>(d + ((c8 ^ (rr & 7)) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-                    *reinterpret_cast<uint4*>(d + (((c8 + 1) ^ (rr & 7)) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
-                }
-                if (!xw && w == 1) {
-                    sm.kscale[st][lane] = c0;
-                    sm.kscale[st][32 + lane] = c1;
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (xw) tc::mbar_arrive(&sm.x_full[st]);
-                    else {
-                        if (w == 1) tc::mbar_arrive(&sm.sc_full[st]);
-                        arrive0(&sm.k_full[st]);
+                    for (int c = 0; c < kPer; ++c) raw[c] = *reinterpret_cast<const uint4*>(sm.ring[st] + (tid + c * kKWarps * 32) * 16);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sm.code_read);
+                    if (w == 1) {                // the stage's earlier scales are spent: it has been free
+                        sm.kscale[st][lane] = sc0;
+                        sm.kscale[st][32 + lane] = sc1;
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&sm.sc_full[st]);
+                        sc0 = at0 ? __ldg(at0) : 0.f;
+                        sc1 = at1 ? __ldg(at1) : 0.f;
+                        at0 = scale_at(i + 2, 0);
+                        at1 = scale_at(i + 2, 1);
                     }
+                    // The widened rows go over the codes: not before every warp holds its own.
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_read, tile & 1, abort_flag));
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst[c], raw[c]);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive0(&sm.k_full[st]);
+                }
+            }
+        } else {
+            constexpr int kPer = 4;              // 32 x 16 / 128
+            const int q = tid & 15, r0 = tid >> 4;               // chunk, and first of the rows r0, r0 + 8, ...
+            const int dst = place(r0, (rank ^ 1) * 16 + q);      // rows 8 apart: a group apart
+            const uint8_t* src = a.kv + rank * 256 + q * 16;
+            const int my0 = (rank ^ 1) * kOwn;
+            while (ok && next_seg(s)) {
+                r += 2;
+                const int n = s.k1 - s.k0;
+                // Lane l: offset of exchanged row l of tile i, -1 behind the context.
+                auto row_at = [&](int i) -> int64_t {
+                    const int key = (s.k0 + i) * kTile + my0 + lane;
+                    if (i >= n || key >= s.len) return -1;
+                    int rw;
+                    const int pg = page_of(s.seq, key, &rw);
+                    return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
+                };
+                auto load = [&](int64_t off, uint4 (&raw)[kPer]) {
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) {
+                        const int64_t ro = __shfl_sync(0xffffffffu, off, r0 + 8 * c);
+                        raw[c] = ro >= 0 ? ldg_nc16(src + ro) : make_uint4(0, 0, 0, 0);
+                    }
+                };
+                uint4 raw[kPer];
+                load(row_at(0), raw);
+                int64_t off = row_at(1);
+                for (int i = 0; i < n; ++i, ++r) {
+                    uint4 cur[kPer];
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) cur[c] = raw[c];
+                    load(off, raw);              // the next tile's codes travel under this one
+                    off = row_at(i + 2);
+                    const int st = r % kStages;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_go[st], (ph >> st) & 1, abort_flag));
+                    ph ^= 1u << st;
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst + c * kGroup, cur[c]);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sm.x_full[st]);
                 }
             }
         }
@@ -941,25 +988,31 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant
     if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
 }
 
-// The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x 8 x `chunks` x 1.
-bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int chunks) {
-    const bool one = a.n_pages == 1 || a.seq_b == 0;
-    const cuuint64_t d[4] = {64, (cuuint64_t)a.page_size, kAtoms, (cuuint64_t)(one ? 1 : a.n_pages)};
-    const cuuint64_t s[3] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
-    const cuuint32_t box[4] = {64, 8, (cuuint32_t)chunks, 1}, e[4] = {1, 1, 1, 1};
-    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(a.kv), d, s, box, e,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+// The cache as (run of dims, rows, runs, pages): 9 runs of 64 BF16 dims (128-byte swizzle) or 3 of 192 codes (none).  Box:
+// 8 rows of `runs` runs.
+bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int runs) {
+    const bool one = a.n_pages == 1 || a.seq_b == 0, fp8 = a.kv_scale != nullptr;
+    const cuuint32_t run = fp8 ? kCodeRun : 64;
+    const cuuint64_t d[4] = {run, (cuuint64_t)a.page_size, kD / run, (cuuint64_t)(one ? 1 : a.n_pages)};
+    const cuuint64_t s[3] = {(cuuint64_t)a.tok_b, (cuuint64_t)run * (fp8 ? 1 : 2), (cuuint64_t)(one ? a.tok_b : a.seq_b)};
+    const cuuint32_t box[4] = {run, 8, (cuuint32_t)runs, 1}, e[4] = {1, 1, 1, 1};
+    return tc::encode_tiled()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<uint8_t*>(a.kv), d, s, box, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// (64 dims, 8 rows, 9 chunks, groups of 8 rows, pages), box 64 x 8 x 9 x 4 x 1: a CTA's keys of a tile, in a stage's order.
+// (run, 8 rows, runs, groups of 8 rows, pages), box run x 8 x every run x 4 x 1: a CTA's keys of a tile, in a stage's order.
 bool make_tile_map(const LatentArgs& a, CUtensorMap* m) {
-    const bool one = a.n_pages == 1 || a.seq_b == 0;
-    const cuuint64_t d[5] = {64, 8, kAtoms, (cuuint64_t)(a.page_size / 8), (cuuint64_t)(one ? 1 : a.n_pages)};
-    const cuuint64_t s[4] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)a.tok_b * 8, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
-    const cuuint32_t box[5] = {64, 8, kAtoms, 4, 1}, e[5] = {1, 1, 1, 1, 1};
-    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(a.kv), d, s, box, e,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+    const bool one = a.n_pages == 1 || a.seq_b == 0, fp8 = a.kv_scale != nullptr;
+    const cuuint32_t run = fp8 ? kCodeRun : 64;
+    const cuuint64_t d[5] = {run, 8, kD / run, (cuuint64_t)(a.page_size / 8), (cuuint64_t)(one ? 1 : a.n_pages)};
+    const cuuint64_t s[4] = {(cuuint64_t)a.tok_b, (cuuint64_t)run * (fp8 ? 1 : 2), (cuuint64_t)a.tok_b * 8,
+                             (cuuint64_t)(one ? a.tok_b : a.seq_b)};
+    const cuuint32_t box[5] = {run, 8, kD / run, 4, 1}, e[5] = {1, 1, 1, 1, 1};
+    return tc::encode_tiled()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                              const_cast<uint8_t*>(a.kv), d, s, box, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1021,11 +1074,13 @@ cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
     // One box per CTA and tile where pages hold 32 rows whole; a sequence without pages may end inside 8 rows, which
     // only the map by single rows bounds.
     k.whole = a.page_size % 32 == 0;
-    if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, kAtoms)) || !make_kv_map(a, &xm, 4)) return cudaErrorInvalidValue;
+    const int runs = a.kv_scale ? kD / kCodeRun : kAtoms;
+    if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, runs))) return cudaErrorInvalidValue;
+    if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
+    if (!make_kv_map(a, &xm, 4)) return cudaErrorInvalidValue;
     return launch_t<false>(qm, km, xm, k, st);
 }
 
