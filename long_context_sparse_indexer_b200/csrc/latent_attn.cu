@@ -28,7 +28,8 @@
 // Warps: 0..3 and 4..7 softmax, alternate tiles (thread = TMEM lane = (row, half of the keys); the two halves of a row
 // exchange their maxima through shared memory), 8 the MMAs (in CTA 0, for both), 9 the plan of the cluster's segments.
 // BF16: 10 and 11 load keys and exchanged rows by TMA.  FP8: 10 loads a tile's codes into the head of the stage that
-// they widen into, 11..16 widen them there and 17..20 the exchanged rows (bit moves and one exact multiply a pair).
+// they widen into, 11..16 widen them there and 17..20 the exchanged rows (bit moves and one exact multiply a pair), 21
+// brings the row scales.
 // All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
 #include <cstring>
@@ -209,7 +210,7 @@ __device__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
 }
 
 template <bool FP8>
-constexpr int kThreadsOf = 32 * (kLoadWarp + (FP8 ? 1 + kKWarps + kXWarps : 2));
+constexpr int kThreadsOf = 32 * (kLoadWarp + (FP8 ? 2 + kKWarps + kXWarps : 2));
 
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
@@ -224,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     volatile int* abort_flag = &sm.abort;
 
     if (threadIdx.x == 0) {
-        constexpr int kLoaders = FP8 ? 1 + kKWarps + kXWarps : 2;
+        constexpr int kLoaders = FP8 ? 2 + kKWarps + kXWarps : 2;
         for (int i = 0; i < kSegs; ++i) {
             tc::mbar_init(&sm.seg_full[i], 1);
             tc::mbar_init(&sm.seg_empty[i], kSoftmaxWarps + kLoaders + (rank == 0 ? 1 : 0));
@@ -804,83 +805,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         }
     } else if (busy && FP8) {
-        // ---------------- FP8: codes to BF16.  First six warps: own keys, from the codes landed in the stage; four: the
-        // exchanged rows, from global memory (the other CTA has brought them into L2)
-        const bool xw = warp > kLoadWarp + kKWarps;
-        const int w = xw ? warp - kLoadWarp - kKWarps - 1 : warp - kLoadWarp - 1, tid = w * 32 + lane;
+        // ---------------- FP8.  Six warps widen the own keys' codes landed in the stage, four the exchanged rows' from global
+        // memory (the other CTA has brought them into L2), one brings the row scales.  A lane takes 8 codes at a time, so
+        // that the 16-byte stores of a warp spread over all banks.
+        const int w = warp - kLoadWarp - 1;
         int r = 0, tile = 0;
         uint32_t ph = 0;                         // parity of each stage's next phase (codes landed; scores done)
         bool ok = true;
         Seg s;
-        auto put = [&](uint8_t* d, uint4 v) {    // 16 codes: two 16-byte chunks next to each other under the swizzle
-            const uint2 w0 = widen4(v.x), w1 = widen4(v.y), w2 = widen4(v.z), w3 = widen4(v.w);
+        auto put = [&](uint8_t* d, uint2 v) {
+            const uint2 w0 = widen4(v.x), w1 = widen4(v.y);
             *reinterpret_cast<uint4*>(d) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>((uintptr_t)d ^ 16)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
         };
-        // Place in a stage of 16 dims (chunk q of the row's 36) of row rr.
-        auto place = [&](int rr, int q) { return (rr >> 3) * kGroup + (q >> 2) * kAtom + (rr & 7) * 128 + ((((q & 3) * 2) ^ (rr & 7)) << 4); };
-        if (!xw) {
-            constexpr int kPer = 6;              // 16-code chunks per thread: 32 x 36 / 192
-            int dst[kPer];
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-                const int i = tid + c * kKWarps * 32, g = i / 288, part = i % 288 / 96, r8 = i % 96 / 12;
-                dst[c] = place(g * 8 + r8, part * 12 + i % 12);
-            }
+        if (w < kKWarps) {
+            // 8-code chunk tid + 192 c of the landed codes: row tid / 24 of group c / 3, chunk tid % 24 of run c % 3.
+            constexpr int kPer = 12;
+            const int tid = w * 32 + lane, r8 = tid / 24, h = tid % 24;
+            const int dst = (h >> 3) * kAtom + r8 * 128 + (((h & 7) ^ r8) << 4);
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
-                // Row scales (second warp; lane l: keys l and l + 32): found two tiles ahead, loaded one ahead.
-                auto scale_at = [&](int i, int hh) -> const float* {
-                    const int key = (s.k0 + i) * kTile + hh * 32 + lane;
-                    if (i >= n || key >= s.len) return nullptr;
-                    int rw;
-                    const int pg = page_of(s.seq, key, &rw);
-                    return pg < 0 ? nullptr : a.kv_scale + pg * a.scale_seq + rw;
-                };
-                const float *at0 = nullptr, *at1 = nullptr;
-                float sc0 = 0.f, sc1 = 0.f;
-                if (w == 1) {
-                    at0 = scale_at(0, 0); at1 = scale_at(0, 1);
-                    if (at0) sc0 = __ldg(at0);
-                    if (at1) sc1 = __ldg(at1);
-                    at0 = scale_at(1, 0); at1 = scale_at(1, 1);
-                }
                 for (int i = 0; i < n; ++i, ++r, ++tile) {
                     const int st = r % kStages;
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_full[st], (ph >> st) & 1, abort_flag));
                     ph ^= 1u << st;
                     if (!ok) break;
-                    uint4 raw[kPer];
+                    uint2 raw[kPer];
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) raw[c] = *reinterpret_cast<const uint4*>(sm.ring[st] + (tid + c * kKWarps * 32) * 16);
+                    for (int c = 0; c < kPer; ++c) raw[c] = *reinterpret_cast<const uint2*>(sm.ring[st] + (tid + c * kKWarps * 32) * 8);
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sm.code_read);
-                    if (w == 1) {                // the stage's earlier scales are spent: it has been free
-                        sm.kscale[st][lane] = sc0;
-                        sm.kscale[st][32 + lane] = sc1;
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&sm.sc_full[st]);
-                        sc0 = at0 ? __ldg(at0) : 0.f;
-                        sc1 = at1 ? __ldg(at1) : 0.f;
-                        at0 = scale_at(i + 2, 0);
-                        at1 = scale_at(i + 2, 1);
-                    }
                     // The widened rows go over the codes: not before every warp holds its own.
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_read, tile & 1, abort_flag));
                     if (!ok) break;
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst[c], raw[c]);
+                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst + (c / 3) * kGroup + (c % 3) * 3 * kAtom, raw[c]);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive0(&sm.k_full[st]);
                 }
             }
-        } else {
-            constexpr int kPer = 4;              // 32 x 16 / 128
-            const int q = tid & 15, r0 = tid >> 4;               // chunk, and first of the rows r0, r0 + 8, ...
-            const int dst = place(r0, (rank ^ 1) * 16 + q);      // rows 8 apart: a group apart
-            const uint8_t* src = a.kv + rank * 256 + q * 16;
+        } else if (w < kKWarps + kXWarps) {
+            // Rows wx, wx + 4, ... of the exchanged 32, lane = 8-code chunk of this CTA's 256 dims.
+            constexpr int kPer = 8;
+            const int wx = w - kKWarps;
+            const uint8_t* src = a.kv + rank * 256 + lane * 8;
+            const int col = ((rank ^ 1) * 4 + (lane >> 3)) * kAtom;
+            const int d0 = col + wx * 128 + (((lane & 7) ^ wx) << 4), d1 = col + (wx + 4) * 128 + (((lane & 7) ^ (wx + 4)) << 4);
             const int my0 = (rank ^ 1) * kOwn;
             while (ok && next_seg(s)) {
                 r += 2;
@@ -893,18 +864,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const int pg = page_of(s.seq, key, &rw);
                     return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
                 };
-                auto load = [&](int64_t off, uint4 (&raw)[kPer]) {
+                auto load = [&](int64_t off, uint2 (&raw)[kPer]) {
 #pragma unroll
                     for (int c = 0; c < kPer; ++c) {
-                        const int64_t ro = __shfl_sync(0xffffffffu, off, r0 + 8 * c);
-                        raw[c] = ro >= 0 ? ldg_nc16(src + ro) : make_uint4(0, 0, 0, 0);
+                        const int64_t ro = __shfl_sync(0xffffffffu, off, wx + 4 * c);
+                        raw[c] = ro >= 0 ? __ldg(reinterpret_cast<const uint2*>(src + ro)) : make_uint2(0, 0);
                     }
                 };
-                uint4 raw[kPer];
+                uint2 raw[kPer];
                 load(row_at(0), raw);
                 int64_t off = row_at(1);
                 for (int i = 0; i < n; ++i, ++r) {
-                    uint4 cur[kPer];
+                    uint2 cur[kPer];
 #pragma unroll
                     for (int c = 0; c < kPer; ++c) cur[c] = raw[c];
                     load(off, raw);              // the next tile's codes travel under this one
@@ -914,10 +885,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     ph ^= 1u << st;
                     if (!ok) break;
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst + c * kGroup, cur[c]);
+                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + (c & 1 ? d1 : d0) + (c >> 1) * kGroup, cur[c]);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sm.x_full[st]);
+                }
+            }
+        } else {
+            // Row scales, lane l: keys l and l + 32; found two tiles ahead, loaded one ahead.
+            while (ok && next_seg(s)) {
+                r += 2;
+                const int n = s.k1 - s.k0;
+                auto scale_at = [&](int i, int hh) -> const float* {
+                    const int key = (s.k0 + i) * kTile + hh * 32 + lane;
+                    if (i >= n || key >= s.len) return nullptr;
+                    int rw;
+                    const int pg = page_of(s.seq, key, &rw);
+                    return pg < 0 ? nullptr : a.kv_scale + pg * a.scale_seq + rw;
+                };
+                const float *at0 = scale_at(0, 0), *at1 = scale_at(0, 1);
+                float n0 = at0 ? __ldg(at0) : 0.f, n1 = at1 ? __ldg(at1) : 0.f;
+                at0 = scale_at(1, 0);
+                at1 = scale_at(1, 1);
+                for (int i = 0; i < n; ++i, ++r) {
+                    const float s0 = n0, s1 = n1;
+                    n0 = at0 ? __ldg(at0) : 0.f;
+                    n1 = at1 ? __ldg(at1) : 0.f;
+                    at0 = scale_at(i + 2, 0);
+                    at1 = scale_at(i + 2, 1);
+                    const int st = r % kStages;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                    if (!ok) break;
+                    sm.kscale[st][lane] = s0;
+                    sm.kscale[st][32 + lane] = s1;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sm.sc_full[st]);
                 }
             }
         }
