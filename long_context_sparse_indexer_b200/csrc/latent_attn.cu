@@ -28,8 +28,7 @@
 // Warps: 0..3 and 4..7 softmax, alternate tiles (thread = TMEM lane = (row, half of the keys); the two halves of a row
 // exchange their maxima through shared memory), 8 the MMAs (in CTA 0, for both), 9 the plan of the cluster's segments.
 // BF16: 10 and 11 load keys and exchanged rows by TMA.  FP8: 10 loads a tile's codes into the head of the stage that
-// they widen into, 11..16 widen them there and 17..20 the exchanged rows (bit moves and one exact multiply a pair), 21
-// brings the row scales.
+// they widen into, 11..18 widen them there and 19..22 the exchanged rows (bit moves only), 23 brings the row scales.
 // All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
 #include <cstring>
@@ -50,14 +49,14 @@ constexpr int kStages = 5, kAtoms = 9, kStageBytes = kAtoms * kOwn * 128;
 constexpr int kAtom = 1024, kGroup = kAtoms * kAtom;
 constexpr int kQAtom = kOwn * 128;               // queries in a stage: 64-dim atoms of 32 rows
 constexpr int kXBytes = 4 * kOwn * 128;
-// FP8: a CTA's codes of a tile land at the head of the stage they widen into, as 8-row groups of three 192-dim runs.
-constexpr int kCodeRun = 192, kCodeGroup = 8 * kD, kCodeBytes = kOwn * kD;
+// FP8: the codes of 8 rows land at the head of the group they widen into, as three 192-dim runs.
+constexpr int kCodeRun = 192, kCodeBytes = kOwn * kD;
 constexpr int kQTmem = 6;                                        // query atoms in TMEM, the others in shared memory
 constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
 constexpr int kMaxClusters = 80;
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kPlanWarp = 9, kLoadWarp = 10;   // from kLoadWarp on: loads
-constexpr int kKWarps = 6, kXWarps = 4;                          // FP8 converters
+constexpr int kKWarps = 8, kXWarps = 4;                          // FP8 converters
 static_assert(kQCol + kQTmem * 32 == 512, "TMEM columns");
 
 struct Seg {
@@ -68,7 +67,7 @@ struct Smem {
     alignas(1024) uint8_t ring[kStages][kStageBytes];
     alignas(1024) uint8_t q[kAtoms - kQTmem][kRows * 128];
     alignas(1024) uint8_t p[2][kRows * 128];
-    float kscale[kStages][kTile];                // FP8: the tile's row scales
+    float kscale[kStages][kTile];                // FP8: the tile's row scales, times kUp
     float mx[2][2][128];                         // what the halves of a row exchange, per warpgroup: tile maxima, sums
     float m_ref[128];                            // the reference maximum after the latest decided tile
     float m_last[2][kRows];                      // each warpgroup's last reference, and its sums by half
@@ -81,7 +80,6 @@ struct Smem {
     uint64_t k_full[kStages];                    // CTA 0: both CTAs' keys have landed
     uint64_t sc_full[kStages];                   // FP8: kscale is written
     uint64_t code_full[kStages];                 // FP8: the stage's codes have landed
-    uint64_t code_read;                          // FP8: every converter of own keys holds its codes in registers
     uint64_t x_go[kStages], x_full[kStages];     // the scores of the stage are done; its exchanged rows have landed
     uint64_t empty[kStages];
     uint64_t q_full, q_ready;                    // queries staged; (CTA 0) moved to their operand places in both CTAs
@@ -157,25 +155,27 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m
         :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v) : "memory");
 }
 // Boxes completing on a barrier of this CTA.
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w, int v) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-        :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v) : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
         :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Four e4m3 codes (a word) to BF16, exactly: the code's exponent and mantissa moved into a BF16's make
-// value * 2^-120 (subnormals included), one multiply by 2^120 restores it.
+// Four e4m3 codes (a word) to BF16 values times 2^-120, exactly (subnormals included): sign, exponent and mantissa moved
+// into place, the exponent keeping e4m3's bias of 7 under BF16's of 127.  The factor is made good by the other operands:
+// queries and row scales carry kUp, and the results 1 / (kUp * 2^-120) = kUp.
+constexpr float kUp = 1152921504606846976.f;     // 2^60
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
-    uint2 r;
-    const uint32_t t0 = __byte_perm(w, 0, 0x1404), t1 = __byte_perm(w, 0, 0x3424);
-    const uint32_t u0 = (t0 & 0x80008000u) | ((t0 >> 4) & 0x07f007f0u), u1 = (t1 & 0x80008000u) | ((t1 >> 4) & 0x07f007f0u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(u0), "r"(0x7b807b80u));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(u1), "r"(0x7b807b80u));
+    // A code's byte below its sign replicated (selectors 8 + i), shifted by 4: sign at bit 15, exponent from bit 7.
+    uint32_t lo, hi;
+    asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(lo) : "r"(w));
+    asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(hi) : "r"(w));
+    return make_uint2((lo << 4) & 0x87f087f0u, (hi << 4) & 0x87f087f0u);
+}
+// Two BF16 values times kUp.
+__device__ __forceinline__ uint32_t up2(uint32_t v) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x5d805d80u));
     return r;
 }
 
@@ -231,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             tc::mbar_init(&sm.seg_empty[i], kSoftmaxWarps + kLoaders + (rank == 0 ? 1 : 0));
         }
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&sm.k_full[i], FP8 ? 2 * kKWarps : 1);
+            tc::mbar_init(&sm.k_full[i], FP8 ? kKWarps : 1);     // FP8: four warps of each CTA
             tc::mbar_init(&sm.sc_full[i], 1);
             tc::mbar_init(&sm.code_full[i], 1);
             tc::mbar_init(&sm.x_go[i], 1);
@@ -239,7 +239,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             tc::mbar_init(&sm.empty[i], 1);
         }
         tc::mbar_init(&sm.q_full, 1);
-        tc::mbar_init(&sm.code_read, kKWarps);
         tc::mbar_init(&sm.q_ready, 2 * kSoftmaxWarps);
         tc::mbar_init(&sm.q_taken, kSoftmaxWarps);
         tc::mbar_init(&sm.o_read, kSoftmaxWarps);
@@ -494,15 +493,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const uint4 v = *reinterpret_cast<const uint4*>(src + at * kQAtom + ((c ^ (row & 7)) << 4));
                     w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
                 }
+                if constexpr (FP8)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) w[c] = up2(w[c]);
                 tc::tmem_st32(tmem + kQCol + at * 32 + lane_off, w);
             }
             // The other atoms keep their swizzle: bytes move as they are, a quarter of a row per thread.
 #pragma unroll
             for (int at = kQTmem; at < kAtoms; ++at)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + 2 * wg + c) * 16) =
-                        *reinterpret_cast<const uint4*>(src + at * kQAtom + (4 * hf + 2 * wg + c) * 16);
+                for (int c = 0; c < 2; ++c) {
+                    uint4 v = *reinterpret_cast<const uint4*>(src + at * kQAtom + (4 * hf + 2 * wg + c) * 16);
+                    if constexpr (FP8) v = make_uint4(up2(v.x), up2(v.y), up2(v.z), up2(v.w));
+                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + 2 * wg + c) * 16) = v;
+                }
             tc::fence_proxy_async_smem();
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -703,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
             if (!alive) break;
             tc::tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l > 0.f ? (FP8 ? kUp : 1.f) / l : 0.f;
             const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
             const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
             const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
@@ -792,11 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (xw) {                        // 256 dims of 8 rows a box
                     if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + (rank ^ 1) * 4 * kAtom, &xmap, &sm.x_full[st], 0, rw, rank * 4, pg);
                 } else if (FP8) {
-                    if (k.whole) {
-                        if (lane == 0) tma_load_5d(sm.ring[st], &kmap, &sm.code_full[st], 0, 0, 0, rw / 8, pg);
-                    } else if (lane < 4) {
-                        tma_load_4d(sm.ring[st] + lane * kCodeGroup, &kmap, &sm.code_full[st], 0, rw, 0, pg);
-                    }
+                    if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup, &kmap, &sm.code_full[st], 0, rw, 0, pg);
                 } else if (k.whole) {            // 32 rows in one box
                     if (lane == 0) tma_load_5d_pair(sm.ring[st], &kmap, bar0, 0, 0, 0, rw / 8, pg);
                 } else if (lane < 4) {           // 8 rows a box
@@ -805,7 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         }
     } else if (busy && FP8) {
-        // ---------------- FP8.  Six warps widen the own keys' codes landed in the stage, four the exchanged rows' from global
+        // ---------------- FP8.  Eight warps widen the own keys' codes landed in the stage, four the exchanged rows' from global
         // memory (the other CTA has brought them into L2), one brings the row scales.  A lane takes 8 codes at a time, so
         // that the 16-byte stores of a warp spread over all banks.
         const int w = warp - kLoadWarp - 1;
@@ -818,28 +818,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             *reinterpret_cast<uint4*>(d) = make_uint4(w0.x, w0.y, w1.x, w1.y);
         };
         if (w < kKWarps) {
-            // 8-code chunk tid + 192 c of the landed codes: row tid / 24 of group c / 3, chunk tid % 24 of run c % 3.
-            constexpr int kPer = 12;
-            const int tid = w * 32 + lane, r8 = tid / 24, h = tid % 24;
-            const int dst = (h >> 3) * kAtom + r8 * 128 + (((h & 7) ^ r8) << 4);
+            // Warps 0..3 take the even tiles, 4..7 the odd ones; warp = 8-row group, which only it reads and writes.  8-code chunk
+            // lane + 32 c: run c / 6, and in it row (lane + 32 (c % 6)) / 24.
+            constexpr int kPer = 18;
+            const int g = w & 3, set = w >> 2;
+            int dst[6];
+#pragma unroll
+            for (int c = 0; c < 6; ++c) {
+                const int r8 = (lane + 32 * c) / 24, h = (lane + 32 * c) % 24;
+                dst[c] = g * kGroup + (h >> 3) * kAtom + r8 * 128 + (((h & 7) ^ r8) << 4);
+            }
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
                 for (int i = 0; i < n; ++i, ++r, ++tile) {
                     const int st = r % kStages;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_full[st], (ph >> st) & 1, abort_flag));
+                    const uint32_t turn = (ph >> st) & 1;
                     ph ^= 1u << st;
+                    // Every tile's stage is waited free for, the other set's too: then no phase of its barriers goes unseen.
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                    if (!ok) break;
+                    if ((tile & 1) != set) continue;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_full[st], turn, abort_flag));
                     if (!ok) break;
                     uint2 raw[kPer];
+                    const uint8_t* src = sm.ring[st] + g * kGroup + lane * 8;
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) raw[c] = *reinterpret_cast<const uint2*>(sm.ring[st] + (tid + c * kKWarps * 32) * 8);
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&sm.code_read);
-                    // The widened rows go over the codes: not before every warp holds its own.
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_read, tile & 1, abort_flag));
-                    if (!ok) break;
+                    for (int c = 0; c < kPer; ++c) raw[c] = *reinterpret_cast<const uint2*>(src + c * 256);
+                    __syncwarp();                // the widened rows go over the codes
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst + (c / 3) * kGroup + (c % 3) * 3 * kAtom, raw[c]);
+                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst[c % 6] + (c / 6) * 3 * kAtom, raw[c]);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive0(&sm.k_full[st]);
@@ -916,8 +924,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const int st = r % kStages;
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                     if (!ok) break;
-                    sm.kscale[st][lane] = s0;
-                    sm.kscale[st][32 + lane] = s1;
+                    sm.kscale[st][lane] = s0 * kUp;
+                    sm.kscale[st][32 + lane] = s1 * kUp;
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sm.sc_full[st]);
                 }
@@ -1004,17 +1012,15 @@ bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int runs) {
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// (run, 8 rows, runs, groups of 8 rows, pages), box run x 8 x every run x 4 x 1: a CTA's keys of a tile, in a stage's order.
+// BF16: (64 dims, 8 rows, 9 chunks, groups of 8 rows, pages), box 64 x 8 x 9 x 4 x 1: a CTA's keys of a tile, in a stage's
+// order.
 bool make_tile_map(const LatentArgs& a, CUtensorMap* m) {
-    const bool one = a.n_pages == 1 || a.seq_b == 0, fp8 = a.kv_scale != nullptr;
-    const cuuint32_t run = fp8 ? kCodeRun : 64;
-    const cuuint64_t d[5] = {run, 8, kD / run, (cuuint64_t)(a.page_size / 8), (cuuint64_t)(one ? 1 : a.n_pages)};
-    const cuuint64_t s[4] = {(cuuint64_t)a.tok_b, (cuuint64_t)run * (fp8 ? 1 : 2), (cuuint64_t)a.tok_b * 8,
-                             (cuuint64_t)(one ? a.tok_b : a.seq_b)};
-    const cuuint32_t box[5] = {run, 8, kD / run, 4, 1}, e[5] = {1, 1, 1, 1, 1};
-    return tc::encode_tiled()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-                              const_cast<uint8_t*>(a.kv), d, s, box, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+    const bool one = a.n_pages == 1 || a.seq_b == 0;
+    const cuuint64_t d[5] = {64, 8, kAtoms, (cuuint64_t)(a.page_size / 8), (cuuint64_t)(one ? 1 : a.n_pages)};
+    const cuuint64_t s[4] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)a.tok_b * 8, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
+    const cuuint32_t box[5] = {64, 8, kAtoms, 4, 1}, e[5] = {1, 1, 1, 1, 1};
+    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(a.kv), d, s, box, e,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1078,7 +1084,7 @@ cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
     }
     // One box per CTA and tile where pages hold 32 rows whole; a sequence without pages may end inside 8 rows, which
     // only the map by single rows bounds.
-    k.whole = a.page_size % 32 == 0;
+    k.whole = !a.kv_scale && a.page_size % 32 == 0;
     const int runs = a.kv_scale ? kD / kCodeRun : kAtoms;
     if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, runs))) return cudaErrorInvalidValue;
     if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);

@@ -431,6 +431,22 @@ def test_latent_peaked_and_extreme_scores(cuda):
         s.check()
 
 
+def test_latent_every_fp8_code_and_far_scales(cuda):
+    """Rows of all 254 finite codes (subnormal ones alone in some), scales from 2^-40 to 2^20, one row far above the others."""
+    finite = torch.tensor([c for c in range(256) if c & 0x7f != 0x7f], dtype=torch.uint8, device=DEV)
+    tiny = torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, 129, 130, 131, 132, 133, 134, 135], dtype=torch.uint8, device=DEV)
+    for top, kind in ((-40, finite), (20, finite), (0, tiny), (12, tiny)):
+        s = Latent(40 + top, 20, [200], [[199]], page=32, fp8=True, scale=1.0 if kind is tiny else 0.02)
+        g = _gen(top + 99)
+        at = (s.pages.table[0].long()[torch.arange(200, device=DEV) // 32], torch.arange(200, device=DEV) % 32)
+        s.cache.data[at] = kind[torch.randint(0, len(kind), (200, 576), generator=g, device=DEV)]
+        s.cache.scale[at] = torch.exp2(top - torch.rand(200, generator=g, device=DEV) * 3)
+        s.sm = 2.0 ** -max(top, 0) / 24
+        s.rows = (s.cache.data.view(E4M3)[at].double() * s.cache.scale[at].double()[:, None])[None]
+        s.run()
+        s.check(top)
+
+
 def test_latent_bad_batch_is_reported(cuda):
     def run(q_seq, q_pos, lens=(30, 30), page=None):
         s = Latent(2, 16, [30, 30], [[29, 29], [29, 29]], page=16, bad_pages=False)
