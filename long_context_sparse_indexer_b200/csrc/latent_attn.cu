@@ -49,13 +49,18 @@ constexpr int kStages = 5, kAtoms = 9, kStageBytes = kAtoms * kOwn * 128;
 constexpr int kAtom = 1024, kGroup = kAtoms * kAtom;
 constexpr int kQAtom = kOwn * 128;               // queries in a stage: 64-dim atoms of 32 rows
 constexpr int kXBytes = 4 * kOwn * 128;
-// FP8: the codes of 8 rows land at the head of the group they widen into, as three 192-dim runs.
-constexpr int kCodeRun = 192, kCodeBytes = kOwn * kD;
+// FP8: the codes of 8 rows land in the tail of the group they widen into, in its order (nine 512-byte atoms), so that
+// widening atom after atom never writes over codes not yet read: 1024 (c + 1) <= 4608 + 512 (c + 1) for c < 9.
+constexpr int kCodeBytes = kOwn * kD, kCodeAt = kGroup / 2;
 constexpr int kQTmem = 6;                                        // query atoms in TMEM, the others in shared memory
 constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
 constexpr int kMaxClusters = 80;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kPlanWarp = 9, kLoadWarp = 10;   // from kLoadWarp on: loads
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8;
+// The other warps.  FP8 (24 warps): the widening warps keep off the scheduler of the MMA warp (warp mod 4 = 0).
+template <bool FP8> constexpr int kPlanWarp = FP8 ? 20 : 9;
+template <bool FP8> constexpr int kLoadWarp = FP8 ? 16 : 10;     // queries and own keys
+template <bool FP8> constexpr int kXWarp = FP8 ? -1 : 11;        // BF16: exchanged rows
 constexpr int kKWarps = 8, kXWarps = 4;                          // FP8 converters
 static_assert(kQCol + kQTmem * 32 == 512, "TMEM columns");
 
@@ -112,6 +117,13 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// A bounded wait whose slow part is a call: the roles' loops together fill the instruction cache otherwise (with every
+// wait inlined and the products issued from three places the FP8 kernel was 140 KB of code, half its time fetching).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) { return tc::mbar_wait(bar, parity, abort); }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return tc::mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
 }
 
 // ---- pair forms of the tcgen05 and mbarrier operations
@@ -186,8 +198,19 @@ struct LatentKernelArgs {
     int whole;                                   // a tile's 32 keys of a CTA are one TMA box (pages of whole 32 rows)
 };
 
+// Page (or sequence, without pages) of a sequence's row and its place in it; -1, reported, for a page outside the pool.
+__device__ __noinline__ int page_of(const LatentArgs& a, int seq, int row, int* in_page) {
+    if (!a.table) { *in_page = row; return seq; }
+    const int pg = row / a.page_size;
+    *in_page = row - pg * a.page_size;
+    const int id = a.table[seq * a.table_ld + pg];
+    if (id >= 0 && id < a.n_pages) return id;
+    report(a.status, LSA_ERR_DEVICE_DATA);
+    return -1;
+}
+
 // Keys that some token of the unit sees (0: padding only), and its sequence.  `tell`: report bad tokens.
-__device__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
+__device__ __noinline__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
     const LatentArgs& a = k.a;
     const int g = u / k.m_tiles, r0 = (u - g * k.m_tiles) * kM, r1 = min(k.group_rows, r0 + kM);
     const int t0 = g * a.q_group, b = a.q_seq[t0];
@@ -210,7 +233,7 @@ __device__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
 }
 
 template <bool FP8>
-constexpr int kThreadsOf = 32 * (kLoadWarp + (FP8 ? 2 + kKWarps + kXWarps : 2));
+constexpr int kThreadsOf = 32 * (FP8 ? 24 : 12);
 
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
@@ -311,31 +334,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     int seg_i = 0;
     auto next_seg = [&](Seg& s) -> bool {
         const int d = seg_i % kSegs;
-        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.seg_full[d], (seg_i / kSegs) & 1, abort_flag));
+        const bool ok = __all_sync(0xffffffffu, wait(&sm.seg_full[d], (seg_i / kSegs) & 1, abort_flag));
         s = sm.seg[d];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.seg_empty[d]);
         ++seg_i;
         return ok && s.unit >= 0;
     };
-    // Byte offset of a sequence's row (pages or not), or -1 for a page outside the pool.
-    auto page_of = [&](int seq, int row, int* in_page) -> int {
-        if (!a.table) { *in_page = row; return seq; }
-        const int pg = row / a.page_size;
-        *in_page = row - pg * a.page_size;
-        const int id = a.table[seq * a.table_ld + pg];
-        if (id >= 0 && id < a.n_pages) return id;
-        report(a.status, LSA_ERR_DEVICE_DATA);
-        return -1;
-    };
-
     // Queries of a segment into the two stages at ring position r (one warp).  The segment before must have taken
     // its own: their barrier counts one phase at a time.
     auto load_q = [&](const Seg& s, int r, int seg) -> bool {
         const int g = s.unit / k.m_tiles, q0 = g * k.group_rows + (s.unit - g * k.m_tiles) * kM + rank * kRows;
-        bool ok = seg == 0 || __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_taken, (seg - 1) & 1, abort_flag));
+        bool ok = seg == 0 || __all_sync(0xffffffffu, wait(&sm.q_taken, (seg - 1) & 1, abort_flag));
         for (int i = 0; i < 2 && ok; ++i) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[(r + i) % kStages], (((r + i) / kStages) + 1) & 1, abort_flag));
+            ok = __all_sync(0xffffffffu, wait(&sm.empty[(r + i) % kStages], (((r + i) / kStages) + 1) & 1, abort_flag));
             if (ok && lane == 0) {
                 if (i == 0) tc::mbar_expect_tx(&sm.q_full, 2 * kStageBytes);
                 tc::tma_load_3d(sm.ring[(r + i) % kStages], &qmap, &sm.q_full, 0, q0 + i * 32, 0);
@@ -344,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         return ok;
     };
 
-    if (warp == kPlanWarp) {
+    if (warp == kPlanWarp<FP8>) {
         // ---------------- plan: the run's segments, then the units that hold padding only
         if (busy) {
             int seg = 0, u = sm.u0, k0 = sm.k0;
@@ -366,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     k0 = 0;
                     left -= s.k1 - s.k0;
                     const int d = seg % kSegs;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
                     if (!ok) break;
                     if (lane == 0) {
                         sm.seg[d] = s;
@@ -378,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (u >= k.units) break;
             }
             const int d = seg % kSegs;
-            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
+            if (ok) ok = __all_sync(0xffffffffu, wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
             if (ok && lane == 0) {
                 sm.seg[d].unit = -1;
                 tc::mbar_arrive(&sm.seg_full[d]);
@@ -411,11 +423,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 r += 2;                          // the queries' stages
                 const int n = s.k1 - s.k0;
                 if (leader) {
-                    ok = tc::mbar_wait(&sm.q_ready, seg & 1, abort_flag);
+                    ok = wait(&sm.q_ready, seg & 1, abort_flag);
                     auto score = [&](int i) {
                         const int st = (r + i) % kStages, bf = (tile + i) & 1;
-                        ok = ok && tc::mbar_wait(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
-                             tc::mbar_wait(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
+                        ok = ok && wait(&sm.s_free[bf], (((tile + i) >> 1) + 1) & 1, abort_flag) &&
+                             wait(&sm.k_full[st], (k_ph >> st) & 1, abort_flag);
                         if (!ok) return;
                         k_ph ^= 1u << st;
                         tc::tc_fence_after();
@@ -434,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     };
                     auto weigh = [&](int i) {
                         const int st = (r + i) % kStages, pb = (tile + i) & 1;
-                        ok = ok && tc::mbar_wait(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
+                        ok = ok && wait(&sm.p_full[pb], ((tile + i) >> 1) & 1, abort_flag);
                         if (!ok) return;
                         tc::tc_fence_after();
                         const uint32_t va = tc::smem_u32(sm.ring[st]), pa = tc::smem_u32(sm.p[pb]);
@@ -451,11 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         commit2(&sm.pv_done[pb]);
                     };
                     // S runs two tiles ahead of P V.
-                    if (ok) score(0);
-                    if (ok && n > 1) score(1);
-                    for (int i = 0; i < n && ok; ++i) {
+#pragma unroll 1
+                    for (int i = -2; i < n && ok; ++i) {
                         if (i + 2 < n) score(i + 2);
-                        if (ok) weigh(i);
+                        if (ok && i >= 0) weigh(i);
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
@@ -466,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             if (leader && any) {                 // drain before TMEM is freed
                 volatile int drain = 0;
                 commit2(&sm.mma_done);
-                tc::mbar_wait(&sm.mma_done, 0, &drain);
+                wait(&sm.mma_done, 0, &drain);
             }
         }
     } else if (busy && warp < kSoftmaxWarps) {
@@ -481,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         // Queries of the next segment from the two stages at ring position r to their operand places; each warpgroup
         // takes half the atoms.
         auto take_q = [&](int r) {
-            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_full, seg & 1, abort_flag));
+            alive = alive && __all_sync(0xffffffffu, wait(&sm.q_full, seg & 1, abort_flag));
             if (!alive) return;
             const uint8_t* src = sm.ring[(r + (row >> 5)) % kStages] + (row & 31) * 128;
 #pragma unroll
@@ -516,7 +527,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 arrive0(&sm.q_ready);
             }
             if (warp == 0) {                     // the stages are free once every warp has read them
-                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_taken, seg & 1, abort_flag));
+                alive = __all_sync(0xffffffffu, wait(&sm.q_taken, seg & 1, abort_flag));
                 if (alive && lane == 0) {
                     tc::mbar_arrive(&sm.empty[r % kStages]);
                     tc::mbar_arrive(&sm.empty[(r + 1) % kStages]);
@@ -530,32 +541,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             sm.mx[wg][bf][L] = v;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.pair[wg][quarter & 1]);
-            alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pair[wg][quarter & 1], swaps & 1, abort_flag));
+            alive = alive && __all_sync(0xffffffffu, wait(&sm.pair[wg][quarter & 1], swaps & 1, abort_flag));
             ++swaps;
             return sm.mx[wg][bf][L ^ 64];
         };
-        bool have = next_seg(s);
-        if (have) take_q(0);
-        while (have && alive) {
-            r += 2;
-            const int n = s.k1 - s.k0, g = s.unit / k.m_tiles, r0 = (s.unit - g * k.m_tiles) * kM + rank * kRows;
-            const int grow = r0 + row;           // row in the group
-            int lim = 0;                         // keys this row sees
-            if (grow < k.group_rows) {
-                const int t = g * a.q_group + grow / a.H, pos = a.q_pos[t];
-                if (pos >= 0 && a.q_seq[t] == s.seq && pos < a.seq_len[s.seq]) lim = pos + 1;
+        // Per segment: its queries, then the epilogue of the one before (so that the new scores run meanwhile), then its tiles.
+        Seg cur;                                 // the segment whose tiles are done
+        int g = 0, grow = 0;                     // its group; this thread's row in it
+        float m = kNegInf, l = 0.f;              // reference maximum this warpgroup last used, its sum
+#pragma unroll 1
+        for (bool first = true; alive; first = false) {
+            const bool have = next_seg(s);
+            int lim = 0;                         // keys this row sees in the new segment
+            if (have) {
+                const int g1 = s.unit / k.m_tiles, row1 = (s.unit - g1 * k.m_tiles) * kM + rank * kRows + row;
+                if (row1 < k.group_rows) {
+                    const int t = g1 * a.q_group + row1 / a.H, pos = a.q_pos[t];
+                    if (pos >= 0 && a.q_seq[t] == s.seq && pos < a.seq_len[s.seq]) lim = pos + 1;
+                }
             }
-            float m = kNegInf, l = 0.f;          // reference maximum this warpgroup last used, its sum
+            if (!first) {
+                // Both warpgroups' sums at the larger of their references; past this barrier both have seen their last scores,
+                // so the queries may be replaced.
+                if (hf == 0) sm.m_last[wg][row] = m;
+                sm.l_last[wg][L] = l;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.both);
+                alive = __all_sync(0xffffffffu, wait(&sm.both, (seg - 1) & 1, abort_flag));
+                if (!alive) break;
+                const float m0 = sm.m_last[0][row], m1 = sm.m_last[1][row];
+                m = fmaxf(m0, m1);
+                l = (m0 == kNegInf ? 0.f : sm.l_last[0][L] * ex2(m0 - m)) + (m1 == kNegInf ? 0.f : sm.l_last[1][L] * ex2(m1 - m));
+                l += swap(l);                        // x + y = y + x: both halves hold the same sum
+            }
+            if (have) take_q(r);
+            if (!alive) break;
+            if (!first) {
+                for (int j = max(0, tile - 2); j < tile; ++j)          // both buffers' last products
+                    alive = alive && __all_sync(0xffffffffu, wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
+                if (!alive) break;
+                tc::tc_fence_after();
+                const float inv = l > 0.f ? (FP8 ? kUp : 1.f) / l : 0.f;
+                const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
+                const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
+                const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
+                const bool f32 = !whole || a.o_f32, write = grow < k.group_rows;
+                const size_t orow = (size_t)g * k.group_rows + grow, srow = (size_t)slot * kM + rank * kRows + row;
+                uint8_t* ws = static_cast<uint8_t*>(a.ws);
+                float* of = whole ? static_cast<float*>(a.o) + orow * kDv : reinterpret_cast<float*>(ws + kWsO) + srow * kDv;
+                uint16_t* ob = static_cast<uint16_t*>(a.o) + orow * kDv;
+                if (hf == 0 && wg == 0 && write) {
+                    if (!whole) reinterpret_cast<float*>(ws + kWsLse)[srow] = lse;
+                    else if (a.lse) a.lse[orow] = lse;
+                }
+#pragma unroll 1
+                for (int c = wg * 128; c < wg * 128 + 128; c += 32) {
+                    uint32_t ov[32];
+                    tc::tmem_ld32(tmem + c + lane_off, ov);
+                    tc::tmem_wait_ld();
+                    if (write) {
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                        if (f32) {
+                            float4* d = reinterpret_cast<float4*>(of + hf * 256 + c);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        } else {
+                            uint4* d = reinterpret_cast<uint4*>(ob + hf * 256 + c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                d[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                                  pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                        }
+                    }
+                    __syncwarp();
+                }
+                // The next segment's first product overwrites O: not before both warpgroups have read theirs.
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.o_read);
+                if (have) alive = alive && __all_sync(0xffffffffu, wait(&sm.o_read, (seg - 1) & 1, abort_flag));
+            }
+            if (!have || !alive) break;
+            cur = s;
+            ++seg;
+            r += 2;
+            const int n = s.k1 - s.k0;
+            g = s.unit / k.m_tiles;
+            grow = (s.unit - g * k.m_tiles) * kM + rank * kRows + row;
+            m = kNegInf;
+            l = 0.f;
             for (int i = (tile ^ wg) & 1; i < n; i += 2) {
                 const int tl = tile + i, st = (r + i) % kStages, key0 = (s.k0 + i) * kTile;
-                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[wg], (tl >> 1) & 1, abort_flag));
+                alive = __all_sync(0xffffffffu, wait(&sm.s_full[wg], (tl >> 1) & 1, abort_flag));
                 if (!alive) break;
                 tc::tc_fence_after();
                 // A stage comes round every kStages tiles; its phases before this tile's are complete, since the tile's keys
                 // replaced a stage whose product was done.
                 const uint32_t turn = (stage_ph >> st ^ i / kStages) & 1;
                 if (FP8) {
-                    alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sc_full[st], turn, abort_flag));
+                    alive = __all_sync(0xffffffffu, wait(&sm.sc_full[st], turn, abort_flag));
                     if (!alive) break;
                 }
                 uint32_t w[32];
@@ -597,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 // one chain over the segment's tiles, handed from one warpgroup to the other.
                 float m_prev = m;
                 if (i > 0) {
-                    alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.hand[wg ^ 1][quarter], hand_ph, abort_flag));
+                    alive = alive && __all_sync(0xffffffffu, wait(&sm.hand[wg ^ 1][quarter], hand_ph, abort_flag));
                     hand_ph ^= 1;
                     m_prev = sm.m_ref[L];
                 }
@@ -638,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 // P into its buffer once the product two tiles ago has read it.
-                if (tl >= 2) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[wg], ((tl >> 1) - 1) & 1, abort_flag));
+                if (tl >= 2) alive = __all_sync(0xffffffffu, wait(&sm.pv_done[wg], ((tl >> 1) - 1) & 1, abort_flag));
                 if (!alive) break;
                 uint8_t* prow = sm.p[wg] + row * 128;
 #pragma unroll
@@ -649,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     // O must hold every product before this tile's: P V of the tile before, whose barrier's earlier phase
                     // (three tiles ago) is complete -- this tile's scores were issued after that product.
                     if (i > 0) {
-                        alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[wg ^ 1], ((tl - 1) >> 1) & 1, abort_flag));
+                        alive = __all_sync(0xffffffffu, wait(&sm.pv_done[wg ^ 1], ((tl - 1) >> 1) & 1, abort_flag));
                         if (!alive) break;
                     }
                     tc::tc_fence_after();
@@ -665,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     tc::tmem_wait_st();
                 }
                 // Not before the tile's value rows are there.
-                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_full[st], turn, abort_flag));
+                alive = __all_sync(0xffffffffu, wait(&sm.x_full[st], turn, abort_flag));
                 if (!alive) break;
                 if (!FP8 && key0 + kTile > s.len) {                // value rows behind the last key: zero
                     const int from = s.len - key0;
@@ -685,73 +771,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             for (int i = n - n % kStages; i < n; ++i) stage_ph ^= 1u << ((r + i) % kStages);
             r += n;
             tile += n;
-            if (!alive) break;
-            // The next segment's queries first, so that its scores run during this one's epilogue.
-            const Seg cur = s;
-            ++seg;
-            have = next_seg(s);
-            // Both warpgroups' sums at the larger of their references; past this barrier both have seen their last scores,
-            // so the queries may be replaced.
-            if (hf == 0) sm.m_last[wg][row] = m;
-            sm.l_last[wg][L] = l;
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.both);
-            alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.both, (seg - 1) & 1, abort_flag));
-            if (!alive) break;
-            const float m0 = sm.m_last[0][row], m1 = sm.m_last[1][row];
-            m = fmaxf(m0, m1);
-            l = (m0 == kNegInf ? 0.f : sm.l_last[0][L] * ex2(m0 - m)) + (m1 == kNegInf ? 0.f : sm.l_last[1][L] * ex2(m1 - m));
-            l += swap(l);                        // x + y = y + x: both halves hold the same sum
-            if (have) take_q(r);
-            for (int j = max(0, tile - 2); j < tile; ++j)          // both buffers' last products
-                alive = alive && __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
-            if (!alive) break;
-            tc::tc_fence_after();
-            const float inv = l > 0.f ? (FP8 ? kUp : 1.f) / l : 0.f;
-            const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
-            const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
-            const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
-            const bool f32 = !whole || a.o_f32, write = grow < k.group_rows;
-            const size_t orow = (size_t)g * k.group_rows + grow, srow = (size_t)slot * kM + rank * kRows + row;
-            uint8_t* ws = static_cast<uint8_t*>(a.ws);
-            float* of = whole ? static_cast<float*>(a.o) + orow * kDv : reinterpret_cast<float*>(ws + kWsO) + srow * kDv;
-            uint16_t* ob = static_cast<uint16_t*>(a.o) + orow * kDv;
-            if (hf == 0 && wg == 0 && write) {
-                if (!whole) reinterpret_cast<float*>(ws + kWsLse)[srow] = lse;
-                else if (a.lse) a.lse[orow] = lse;
-            }
-#pragma unroll 1
-            for (int c = wg * 128; c < wg * 128 + 128; c += 32) {
-                uint32_t ov[32];
-                tc::tmem_ld32(tmem + c + lane_off, ov);
-                tc::tmem_wait_ld();
-                if (write) {
-                    float f[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
-                    if (f32) {
-                        float4* d = reinterpret_cast<float4*>(of + hf * 256 + c);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                    } else {
-                        uint4* d = reinterpret_cast<uint4*>(ob + hf * 256 + c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            d[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                              pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-                    }
-                }
-                __syncwarp();
-            }
-            // The next segment's first product overwrites O: not before both warpgroups have read theirs.
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.o_read);
-            if (have) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_read, (seg - 1) & 1, abort_flag));
         }
-    } else if (busy && warp < kLoadWarp + (FP8 ? 1 : 2)) {
+    } else if (busy && (warp == kLoadWarp<FP8> || warp == kXWarp<FP8>)) {
         // ---------------- TMA loads.  First warp: queries and own keys (FP8: their codes); second: the exchanged value rows
-        const bool xw = !FP8 && warp == kLoadWarp + 1;
+        const bool xw = warp == kXWarp<FP8>;
         const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;      // first key in a tile of the rows this warp loads
         int r = 0, seg = 0;
         uint32_t go_ph = 0;
@@ -766,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 const int key = (s.k0 + base + lane / 4) * kTile + my0 + (lane % 4) * 8;
                 *in_page = 0;
                 if (base + lane / 4 >= n || key >= s.len) return a.n_pages;        // outside the map: zeros
-                const int pg = page_of(s.seq, key, in_page);
+                const int pg = page_of(a, s.seq, key, in_page);
                 // Sequences that share their rows (stride 0) are one in the map.
                 return pg < 0 ? a.n_pages : (a.table || a.seq_b ? pg : 0);
             };
@@ -779,10 +802,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 const int st = r % kStages;
                 if (xw) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.x_go[st], (go_ph >> st) & 1, abort_flag));
                     go_ph ^= 1u << st;
                 } else {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                 }
                 if (!ok) break;
                 const uint32_t bar0 = tc::peer_smem(&sm.k_full[st], 0);
@@ -796,7 +819,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (xw) {                        // 256 dims of 8 rows a box
                     if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + (rank ^ 1) * 4 * kAtom, &xmap, &sm.x_full[st], 0, rw, rank * 4, pg);
                 } else if (FP8) {
-                    if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup, &kmap, &sm.code_full[st], 0, rw, 0, pg);
+                    if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + kCodeAt, &kmap, &sm.code_full[st], 0, rw, 0, pg);
                 } else if (k.whole) {            // 32 rows in one box
                     if (lane == 0) tma_load_5d_pair(sm.ring[st], &kmap, bar0, 0, 0, 0, rw / 8, pg);
                 } else if (lane < 4) {           // 8 rows a box
@@ -808,7 +831,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         // ---------------- FP8.  Eight warps widen the own keys' codes landed in the stage, four the exchanged rows' from global
         // memory (the other CTA has brought them into L2), one brings the row scales.  A lane takes 8 codes at a time, so
         // that the 16-byte stores of a warp spread over all banks.
-        const int w = warp - kLoadWarp - 1;
+        // Warps 9, 13, 17, 21 and 10, 14, 18, 22: own keys; 11, 15, 19, 23: exchanged rows.
+        const int role = warp & 3, nth = (warp - 8) >> 2;
+        const int w = role == 0 ? kKWarps + kXWarps : (role - 1) * 4 + nth;
         int r = 0, tile = 0;
         uint32_t ph = 0;                         // parity of each stage's next phase (codes landed; scores done)
         bool ok = true;
@@ -818,16 +843,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             *reinterpret_cast<uint4*>(d) = make_uint4(w0.x, w0.y, w1.x, w1.y);
         };
         if (w < kKWarps) {
-            // Warps 0..3 take the even tiles, 4..7 the odd ones; warp = 8-row group, which only it reads and writes.  8-code chunk
-            // lane + 32 c: run c / 6, and in it row (lane + 32 (c % 6)) / 24.
-            constexpr int kPer = 18;
-            const int g = w & 3, set = w >> 2;
-            int dst[6];
-#pragma unroll
-            for (int c = 0; c < 6; ++c) {
-                const int r8 = (lane + 32 * c) / 24, h = (lane + 32 * c) % 24;
-                dst[c] = g * kGroup + (h >> 3) * kAtom + r8 * 128 + (((h & 7) ^ r8) << 4);
-            }
+            // Warps 0..3 take the even tiles, 4..7 the odd ones; warp = 8-row group, which only it reads and writes.  Lane: 16
+            // codes of an atom, row lane / 4.
+            const int g = w & 3, set = w >> 2, r8 = lane >> 2;
+            const int src = g * kGroup + kCodeAt + lane * 16, dst = g * kGroup + r8 * 128 + (((lane & 3) * 2 ^ r8) << 4);
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
@@ -836,18 +855,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const uint32_t turn = (ph >> st) & 1;
                     ph ^= 1u << st;
                     // Every tile's stage is waited free for, the other set's too: then no phase of its barriers goes unseen.
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                     if (!ok) break;
                     if ((tile & 1) != set) continue;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.code_full[st], turn, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.code_full[st], turn, abort_flag));
                     if (!ok) break;
-                    uint2 raw[kPer];
-                    const uint8_t* src = sm.ring[st] + g * kGroup + lane * 8;
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) raw[c] = *reinterpret_cast<const uint2*>(src + c * 256);
-                    __syncwarp();                // the widened rows go over the codes
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + dst[c % 6] + (c / 6) * 3 * kAtom, raw[c]);
+                    const uint8_t* from = sm.ring[st] + src;
+                    uint8_t* to = sm.ring[st] + dst;
+                    uint4 next = *reinterpret_cast<const uint4*>(from);
+#pragma unroll 1                                 // a small loop: the roles share the instruction caches
+                    for (int c = 0; c < kAtoms; ++c) {
+                        const uint4 v = next;
+                        if (c + 1 < kAtoms) next = *reinterpret_cast<const uint4*>(from + (c + 1) * (kAtom / 2));
+                        __syncwarp();            // atom c + 1 is read before atom c is written
+                        put(to + c * kAtom, make_uint2(v.x, v.y));
+                        put(reinterpret_cast<uint8_t*>((uintptr_t)(to + c * kAtom) ^ 16), make_uint2(v.z, v.w));
+                    }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive0(&sm.k_full[st]);
@@ -869,7 +892,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const int key = (s.k0 + i) * kTile + my0 + lane;
                     if (i >= n || key >= s.len) return -1;
                     int rw;
-                    const int pg = page_of(s.seq, key, &rw);
+                    const int pg = page_of(a, s.seq, key, &rw);
                     return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
                 };
                 auto load = [&](int64_t off, uint2 (&raw)[kPer]) {
@@ -889,7 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     load(off, raw);              // the next tile's codes travel under this one
                     off = row_at(i + 2);
                     const int st = r % kStages;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.x_go[st], (ph >> st) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.x_go[st], (ph >> st) & 1, abort_flag));
                     ph ^= 1u << st;
                     if (!ok) break;
 #pragma unroll
@@ -908,7 +931,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const int key = (s.k0 + i) * kTile + hh * 32 + lane;
                     if (i >= n || key >= s.len) return nullptr;
                     int rw;
-                    const int pg = page_of(s.seq, key, &rw);
+                    const int pg = page_of(a, s.seq, key, &rw);
                     return pg < 0 ? nullptr : a.kv_scale + pg * a.scale_seq + rw;
                 };
                 const float *at0 = scale_at(0, 0), *at1 = scale_at(0, 1);
@@ -922,7 +945,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     at0 = scale_at(i + 2, 0);
                     at1 = scale_at(i + 2, 1);
                     const int st = r % kStages;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                    ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                     if (!ok) break;
                     sm.kscale[st][lane] = s0 * kUp;
                     sm.kscale[st][32 + lane] = s1 * kUp;
@@ -998,14 +1021,12 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant
     if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
 }
 
-// The cache as (run of dims, rows, runs, pages): 9 runs of 64 BF16 dims (128-byte swizzle) or 3 of 192 codes (none).  Box:
-// 8 rows of `runs` runs.
-bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int runs) {
+// The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x 8 x `chunks` x 1; BF16 under the 128-byte swizzle, codes plain.
+bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int chunks) {
     const bool one = a.n_pages == 1 || a.seq_b == 0, fp8 = a.kv_scale != nullptr;
-    const cuuint32_t run = fp8 ? kCodeRun : 64;
-    const cuuint64_t d[4] = {run, (cuuint64_t)a.page_size, kD / run, (cuuint64_t)(one ? 1 : a.n_pages)};
-    const cuuint64_t s[3] = {(cuuint64_t)a.tok_b, (cuuint64_t)run * (fp8 ? 1 : 2), (cuuint64_t)(one ? a.tok_b : a.seq_b)};
-    const cuuint32_t box[4] = {run, 8, (cuuint32_t)runs, 1}, e[4] = {1, 1, 1, 1};
+    const cuuint64_t d[4] = {64, (cuuint64_t)a.page_size, kAtoms, (cuuint64_t)(one ? 1 : a.n_pages)};
+    const cuuint64_t s[3] = {(cuuint64_t)a.tok_b, (cuuint64_t)(fp8 ? 64 : 128), (cuuint64_t)(one ? a.tok_b : a.seq_b)};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)chunks, 1}, e[4] = {1, 1, 1, 1};
     return tc::encode_tiled()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                               const_cast<uint8_t*>(a.kv), d, s, box, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -1085,8 +1106,7 @@ cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
     // One box per CTA and tile where pages hold 32 rows whole; a sequence without pages may end inside 8 rows, which
     // only the map by single rows bounds.
     k.whole = !a.kv_scale && a.page_size % 32 == 0;
-    const int runs = a.kv_scale ? kD / kCodeRun : kAtoms;
-    if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, runs))) return cudaErrorInvalidValue;
+    if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, kAtoms))) return cudaErrorInvalidValue;
     if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
     if (!make_kv_map(a, &xm, 4)) return cudaErrorInvalidValue;
     return launch_t<false>(qm, km, xm, k, st);
