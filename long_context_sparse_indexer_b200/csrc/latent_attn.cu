@@ -887,30 +887,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
-                // Lane l: offset of exchanged row l of tile i, -1 behind the context.
-                auto row_at = [&](int i) -> int64_t {
-                    const int key = (s.k0 + i) * kTile + my0 + lane;
-                    if (i >= n || key >= s.len) return -1;
+                // Lane l: offset of 8-row group l % 4 of tile base + l / 4, -1 behind the context; 8 tiles at a time, a batch ahead.
+                auto fetch = [&](int base) -> int64_t {
+                    const int key = (s.k0 + base + lane / 4) * kTile + my0 + (lane % 4) * 8;
+                    if (base + lane / 4 >= n || key >= s.len) return -1;
                     int rw;
                     const int pg = page_of(a, s.seq, key, &rw);
                     return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
                 };
-                auto load = [&](int64_t off, uint2 (&raw)[kPer]) {
+                int64_t at = fetch(0), at_next = fetch(8);
+                uint2 raw[kPer];
+                auto load = [&](int i) {         // tile i's codes: group c / 2, row wx or wx + 4 of it
+                    if (i % 8 == 0 && i > 0) {
+                        at = at_next;
+                        at_next = fetch(i + 8);
+                    }
+                    const int left = s.len - ((s.k0 + i) * kTile + my0 + wx);      // rows of this warp's residue before the end
 #pragma unroll
                     for (int c = 0; c < kPer; ++c) {
-                        const int64_t ro = __shfl_sync(0xffffffffu, off, wx + 4 * c);
-                        raw[c] = ro >= 0 ? __ldg(reinterpret_cast<const uint2*>(src + ro)) : make_uint2(0, 0);
+                        const int64_t o = __shfl_sync(0xffffffffu, at, (i % 8) * 4 + c / 2);
+                        raw[c] = i < n && o >= 0 && 4 * c < left ? __ldg(reinterpret_cast<const uint2*>(src + o + (wx + 4 * (c & 1)) * a.tok_b))
+                                                                 : make_uint2(0, 0);
                     }
                 };
-                uint2 raw[kPer];
-                load(row_at(0), raw);
-                int64_t off = row_at(1);
+                load(0);
                 for (int i = 0; i < n; ++i, ++r) {
                     uint2 cur[kPer];
 #pragma unroll
                     for (int c = 0; c < kPer; ++c) cur[c] = raw[c];
-                    load(off, raw);              // the next tile's codes travel under this one
-                    off = row_at(i + 2);
+                    load(i + 1);                 // the next tile's codes travel under this one
                     const int st = r % kStages;
                     ok = __all_sync(0xffffffffu, wait(&sm.x_go[st], (ph >> st) & 1, abort_flag));
                     ph ^= 1u << st;
@@ -923,27 +928,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
             }
         } else {
-            // Row scales, lane l: keys l and l + 32; found two tiles ahead, loaded one ahead.
+            // Row scales, lane l: keys l and l + 32, loaded a tile ahead.
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
-                auto scale_at = [&](int i, int hh) -> const float* {
-                    const int key = (s.k0 + i) * kTile + hh * 32 + lane;
-                    if (i >= n || key >= s.len) return nullptr;
+                // Lane l: index of the first scale of 8-row group l % 8 of tile base + l / 8; 4 tiles at a time, a batch ahead.
+                auto fetch = [&](int base) -> int64_t {
+                    const int key = (s.k0 + base + lane / 8) * kTile + (lane % 8) * 8;
+                    if (base + lane / 8 >= n || key >= s.len) return -1;
                     int rw;
                     const int pg = page_of(a, s.seq, key, &rw);
-                    return pg < 0 ? nullptr : a.kv_scale + pg * a.scale_seq + rw;
+                    return pg < 0 ? -1 : pg * a.scale_seq + rw;
                 };
-                const float *at0 = scale_at(0, 0), *at1 = scale_at(0, 1);
-                float n0 = at0 ? __ldg(at0) : 0.f, n1 = at1 ? __ldg(at1) : 0.f;
-                at0 = scale_at(1, 0);
-                at1 = scale_at(1, 1);
+                int64_t at = fetch(0), at_next = fetch(4);
+                float n0 = 0.f, n1 = 0.f;
+                auto load = [&](int i) {
+                    if (i % 4 == 0 && i > 0) {
+                        at = at_next;
+                        at_next = fetch(i + 4);
+                    }
+                    const int left = s.len - (s.k0 + i) * kTile;
+                    const int64_t o0 = __shfl_sync(0xffffffffu, at, (i % 4) * 8 + lane / 8), o1 = __shfl_sync(0xffffffffu, at, (i % 4) * 8 + 4 + lane / 8);
+                    n0 = i < n && o0 >= 0 && lane < left ? __ldg(a.kv_scale + o0 + lane % 8) : 0.f;
+                    n1 = i < n && o1 >= 0 && lane + 32 < left ? __ldg(a.kv_scale + o1 + lane % 8) : 0.f;
+                };
+                load(0);
                 for (int i = 0; i < n; ++i, ++r) {
                     const float s0 = n0, s1 = n1;
-                    n0 = at0 ? __ldg(at0) : 0.f;
-                    n1 = at1 ? __ldg(at1) : 0.f;
-                    at0 = scale_at(i + 2, 0);
-                    at1 = scale_at(i + 2, 1);
+                    load(i + 1);
                     const int st = r % kStages;
                     ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                     if (!ok) break;
