@@ -72,7 +72,7 @@ struct Smem {
     alignas(1024) uint8_t ring[kStages][kStageBytes];
     alignas(1024) uint8_t q[kAtoms - kQTmem][kRows * 128];
     alignas(1024) uint8_t p[2][kRows * 128];
-    float kscale[kStages][kTile];                // FP8: the tile's row scales, times kUp
+    float kscale[kStages][kTile];                // FP8: the tile's row scales, times kUp and the softmax scale
     float mx[2][2][128];                         // what the halves of a row exchange, per warpgroup: tile maxima, sums
     float m_ref[128];                            // the reference maximum after the latest decided tile
     float m_last[2][kRows];                      // each warpgroup's last reference, and its sums by half
@@ -84,7 +84,7 @@ struct Smem {
     uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t k_full[kStages];                    // CTA 0: both CTAs' keys have landed
     uint64_t sc_full[kStages];                   // FP8: kscale is written
-    uint64_t code_full[kStages];                 // FP8: the stage's codes have landed
+    uint64_t code_full[kStages], x_code[4];      // FP8: the stage's codes have landed; those of exchanged group g
     uint64_t x_go[kStages], x_full[kStages];     // the scores of the stage are done; its exchanged rows have landed
     uint64_t empty[kStages];
     uint64_t q_full, q_ready;                    // queries staged; (CTA 0) moved to their operand places in both CTAs
@@ -175,7 +175,8 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uin
 
 // Four e4m3 codes (a word) to BF16 values times 2^-120, exactly (subnormals included): sign, exponent and mantissa moved
 // into place, the exponent keeping e4m3's bias of 7 under BF16's of 127.  The factor is made good by the other operands:
-// queries and row scales carry kUp, and the results 1 / (kUp * 2^-120) = kUp.
+// queries and row scales carry kUp, and the results 1 / (kUp * 2^-120) = kUp.  (The row scales also
+// carry the softmax scale, for the scores; the results give it back.)
 constexpr float kUp = 1152921504606846976.f;     // 2^60
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
     // A code's byte below its sign replicated (selectors 8 + i), shifted by 4: sign at bit 15, exponent from bit 7.
@@ -266,6 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         tc::mbar_init(&sm.q_taken, kSoftmaxWarps);
         tc::mbar_init(&sm.o_read, kSoftmaxWarps);
         tc::mbar_init(&sm.both, kSoftmaxWarps);
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&sm.x_code[i], 1);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sm.s_full[i], 1);
             tc::mbar_init(&sm.s_free[i], 8);
@@ -581,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     alive = alive && __all_sync(0xffffffffu, wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
                 if (!alive) break;
                 tc::tc_fence_after();
-                const float inv = l > 0.f ? (FP8 ? kUp : 1.f) / l : 0.f;
+                const float inv = l > 0.f ? (FP8 ? kUp / a.sm_scale_log2 : 1.f) / l : 0.f;
                 const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
                 const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
                 const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
@@ -659,10 +661,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 v = ks[e];
-                        x[4 * e + 0] = __uint_as_float(w[4 * e + 0]) * (v.x * a.sm_scale_log2);
-                        x[4 * e + 1] = __uint_as_float(w[4 * e + 1]) * (v.y * a.sm_scale_log2);
-                        x[4 * e + 2] = __uint_as_float(w[4 * e + 2]) * (v.z * a.sm_scale_log2);
-                        x[4 * e + 3] = __uint_as_float(w[4 * e + 3]) * (v.w * a.sm_scale_log2);
+                        x[4 * e + 0] = __uint_as_float(w[4 * e + 0]) * v.x;
+                        x[4 * e + 1] = __uint_as_float(w[4 * e + 1]) * v.y;
+                        x[4 * e + 2] = __uint_as_float(w[4 * e + 2]) * v.z;
+                        x[4 * e + 3] = __uint_as_float(w[4 * e + 3]) * v.w;
                     }
                 } else {
 #pragma unroll
@@ -715,10 +717,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     p.y = ex2(p.y);
                     sum[e & 1].x += p.x;
                     sum[e & 1].y += p.y;
-                    if constexpr (FP8) {                           // the row's scale goes into its weight (a masked row's may be anything)
+                    if constexpr (FP8) {                           // the row's scale goes into its weight
                         const float2 v = vs[e];
-                        p.x = p.x > 0.f ? p.x * v.x : 0.f;
-                        p.y = p.y > 0.f ? p.y * v.y : 0.f;
+                        p.x *= v.x;
+                        p.y *= v.y;
                     }
                     pw[e] = pack_bf16x2(p.x, p.y);
                 }
@@ -828,9 +830,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         }
     } else if (busy && FP8) {
-        // ---------------- FP8.  Eight warps widen the own keys' codes landed in the stage, four the exchanged rows' from global
-        // memory (the other CTA has brought them into L2), one brings the row scales.  A lane takes 8 codes at a time, so
-        // that the 16-byte stores of a warp spread over all banks.
+        // ---------------- FP8.  Eight warps widen the own keys' codes landed in the stage, four the exchanged rows', one brings
+        // the row scales.
         // Warps 9, 13, 17, 21 and 10, 14, 18, 22: own keys; 11, 15, 19, 23: exchanged rows.
         const int role = warp & 3, nth = (warp - 8) >> 2;
         const int w = role == 0 ? kKWarps + kXWarps : (role - 1) * 4 + nth;
@@ -838,9 +839,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         uint32_t ph = 0;                         // parity of each stage's next phase (codes landed; scores done)
         bool ok = true;
         Seg s;
-        auto put = [&](uint8_t* d, uint2 v) {
-            const uint2 w0 = widen4(v.x), w1 = widen4(v.y);
-            *reinterpret_cast<uint4*>(d) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+        // n atoms of codes at `from` to n atoms at `to` (this lane's 16 codes of each).
+        auto widen = [&](const uint8_t* from, uint8_t* to, int n) {
+            uint8_t* to2 = reinterpret_cast<uint8_t*>((uintptr_t)to ^ 16);         // the next 8 dims under the swizzle
+            uint4 next = *reinterpret_cast<const uint4*>(from);
+#pragma unroll 1                                 // a small loop: the roles share the instruction caches
+            for (int c = 0; c < n; ++c) {
+                const uint4 v = next;
+                from += kAtom / 2;
+                if (c + 1 < n) next = *reinterpret_cast<const uint4*>(from);
+                __syncwarp();                    // atom c + 1 is read before atom c is written
+                const uint2 w0 = widen4(v.x), w1 = widen4(v.y), w2 = widen4(v.z), w3 = widen4(v.w);
+                *reinterpret_cast<uint4*>(to) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                *reinterpret_cast<uint4*>(to2) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+                to += kAtom;
+                to2 += kAtom;
+            }
         };
         if (w < kKWarps) {
             // Warps 0..3 take the even tiles, 4..7 the odd ones; warp = 8-row group, which only it reads and writes.  Lane: 16
@@ -860,68 +874,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     if ((tile & 1) != set) continue;
                     ok = __all_sync(0xffffffffu, wait(&sm.code_full[st], turn, abort_flag));
                     if (!ok) break;
-                    const uint8_t* from = sm.ring[st] + src;
-                    uint8_t* to = sm.ring[st] + dst;
-                    uint4 next = *reinterpret_cast<const uint4*>(from);
-#pragma unroll 1                                 // a small loop: the roles share the instruction caches
-                    for (int c = 0; c < kAtoms; ++c) {
-                        const uint4 v = next;
-                        if (c + 1 < kAtoms) next = *reinterpret_cast<const uint4*>(from + (c + 1) * (kAtom / 2));
-                        __syncwarp();            // atom c + 1 is read before atom c is written
-                        put(to + c * kAtom, make_uint2(v.x, v.y));
-                        put(reinterpret_cast<uint8_t*>((uintptr_t)(to + c * kAtom) ^ 16), make_uint2(v.z, v.w));
-                    }
+                    widen(sm.ring[st] + src, sm.ring[st] + dst, kAtoms);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive0(&sm.k_full[st]);
                 }
             }
         } else if (w < kKWarps + kXWarps) {
-            // Rows wx, wx + 4, ... of the exchanged 32, lane = 8-code chunk of this CTA's 256 dims.
-            constexpr int kPer = 8;
-            const int wx = w - kKWarps;
-            const uint8_t* src = a.kv + rank * 256 + lane * 8;
-            const int col = ((rank ^ 1) * 4 + (lane >> 3)) * kAtom;
-            const int d0 = col + wx * 128 + (((lane & 7) ^ wx) << 4), d1 = col + (wx + 4) * 128 + (((lane & 7) ^ (wx + 4)) << 4);
-            const int my0 = (rank ^ 1) * kOwn;
+            // Warp = 8-row group of the exchanged rows: once the scores have read the dims that they replace, their codes land
+            // in the tail of that place (the other CTA has brought them into L2) and widen as the keys do, four atoms.
+            const int g = w - kKWarps, r8 = lane >> 2;
+            const int at = g * kGroup + (rank ^ 1) * 4 * kAtom;
+            const int src = at + 2 * kAtom + lane * 16, dst = at + r8 * 128 + (((lane & 3) * 2 ^ r8) << 4);
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
-                // Lane l: offset of 8-row group l % 4 of tile base + l / 4, -1 behind the context; 8 tiles at a time, a batch ahead.
-                auto fetch = [&](int base) -> int64_t {
-                    const int key = (s.k0 + base + lane / 4) * kTile + my0 + (lane % 4) * 8;
-                    if (base + lane / 4 >= n || key >= s.len) return -1;
-                    int rw;
-                    const int pg = page_of(a, s.seq, key, &rw);
-                    return pg < 0 ? -1 : pg * a.seq_b + rw * a.tok_b;
+                // Lane l: page and row of the group in tile base + l.
+                auto fetch = [&](int base, int* row) -> int {
+                    const int key = (s.k0 + base + lane) * kTile + (rank ^ 1) * kOwn + g * 8;
+                    *row = 0;
+                    if (base + lane >= n || key >= s.len) return a.n_pages;        // outside the map: zeros
+                    const int pg = page_of(a, s.seq, key, row);
+                    return pg < 0 ? a.n_pages : (a.table || a.seq_b ? pg : 0);
                 };
-                int64_t at = fetch(0), at_next = fetch(8);
-                uint2 raw[kPer];
-                auto load = [&](int i) {         // tile i's codes: group c / 2, row wx or wx + 4 of it
-                    if (i % 8 == 0 && i > 0) {
-                        at = at_next;
-                        at_next = fetch(i + 8);
+                int nrow, npg = fetch(0, &nrow), crow = 0, cpg = 0;
+                for (int i = 0; i < n; ++i, ++r, ++tile) {
+                    if (i % 32 == 0) {
+                        crow = nrow; cpg = npg;
+                        npg = fetch(i + 32, &nrow);
                     }
-                    const int left = s.len - ((s.k0 + i) * kTile + my0 + wx);      // rows of this warp's residue before the end
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) {
-                        const int64_t o = __shfl_sync(0xffffffffu, at, (i % 8) * 4 + c / 2);
-                        raw[c] = i < n && o >= 0 && 4 * c < left ? __ldg(reinterpret_cast<const uint2*>(src + o + (wx + 4 * (c & 1)) * a.tok_b))
-                                                                 : make_uint2(0, 0);
-                    }
-                };
-                load(0);
-                for (int i = 0; i < n; ++i, ++r) {
-                    uint2 cur[kPer];
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) cur[c] = raw[c];
-                    load(i + 1);                 // the next tile's codes travel under this one
                     const int st = r % kStages;
                     ok = __all_sync(0xffffffffu, wait(&sm.x_go[st], (ph >> st) & 1, abort_flag));
                     ph ^= 1u << st;
                     if (!ok) break;
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) put(sm.ring[st] + (c & 1 ? d1 : d0) + (c >> 1) * kGroup, cur[c]);
+                    if (lane == i % 32) {
+                        tc::mbar_expect_tx(&sm.x_code[g], 4 * kAtom / 2);
+                        tma_load_4d(sm.ring[st] + at + 2 * kAtom, &xmap, &sm.x_code[g], 0, crow, rank * 4, cpg);
+                    }
+                    ok = __all_sync(0xffffffffu, wait(&sm.x_code[g], tile & 1, abort_flag));
+                    if (!ok) break;
+                    widen(sm.ring[st] + src, sm.ring[st] + dst, 4);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sm.x_full[st]);
@@ -929,6 +921,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         } else {
             // Row scales, lane l: keys l and l + 32, loaded a tile ahead.
+            const float up = kUp * a.sm_scale_log2;
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
@@ -959,8 +952,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     const int st = r % kStages;
                     ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
                     if (!ok) break;
-                    sm.kscale[st][lane] = s0 * kUp;
-                    sm.kscale[st][32 + lane] = s1 * kUp;
+                    sm.kscale[st][lane] = s0 * up;
+                    sm.kscale[st][32 + lane] = s1 * up;
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sm.sc_full[st]);
                 }
@@ -1119,8 +1112,8 @@ cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
     // only the map by single rows bounds.
     k.whole = !a.kv_scale && a.page_size % 32 == 0;
     if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, kAtoms))) return cudaErrorInvalidValue;
-    if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
     if (!make_kv_map(a, &xm, 4)) return cudaErrorInvalidValue;
+    if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
     return launch_t<false>(qm, km, xm, k, st);
 }
 
