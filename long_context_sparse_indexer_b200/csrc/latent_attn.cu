@@ -96,7 +96,6 @@ struct Smem {
     uint64_t o_read;                             // every softmax warp has read O
     uint64_t q_taken;                            // every softmax warp has read the staged queries
     uint64_t mma_done;
-    int u0, k0;                                  // where the cluster's run starts
     uint32_t tmem_base;
     int abort;
 };
@@ -112,6 +111,15 @@ constexpr size_t kWsO = 4096;
 constexpr size_t kWsLse = kWsO + (size_t)2 * kMaxClusters * kM * kDv * 4;
 constexpr size_t kWsBytes = kWsLse + (size_t)2 * kMaxClusters * kM * 4;
 static_assert(sizeof(WsHeader) <= kWsO, "header");
+
+// A slot's partial result for a CTA's rows, as the softmax threads hold it: [4-dim group of 64][TMEM lane] float4, lane L = row
+// L & 63 and dims 256 (L >> 6) + 4 group .. + 3.
+__device__ __forceinline__ float4* part_o(void* ws, int slot, int rank) {
+    return reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + kWsO) + ((size_t)slot * 2 + rank) * (kRows * kDv / 4);
+}
+__device__ __forceinline__ float* part_lse(void* ws, int slot) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsLse) + (size_t)slot * kM;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -310,25 +318,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     if (busy && before <= lo && lo < before + mine) {              // one thread: the run starts among its units
         long long at = before;
         for (int u = ua; u < ub; ++u) {
-            int seq;
-            const int n = (unit_len(k, u, &seq, false) + kTile - 1) / kTile;
-            if (lo < at + n) {
-                sm.u0 = u;
-                sm.k0 = (int)(lo - at);
+            Seg s;
+            s.len = unit_len(k, u, &s.seq, false);
+            s.n = (s.len + kTile - 1) / kTile;
+            if (lo < at + s.n) {                 // and publishes the first segment at once
+                s.unit = u;
+                s.k0 = (int)(lo - at);
+                s.k1 = (int)min((long long)s.n, s.k0 + hi - lo);
+                sm.seg[0] = s;
+                tc::mbar_arrive(&sm.seg_full[0]);
                 if (rank == 0) {
                     WsHeader* w = static_cast<WsHeader*>(a.ws);
                     w->unit[cluster] = u;
-                    w->k0[cluster] = sm.k0;
+                    w->k0[cluster] = s.k0;
                 }
                 break;
             }
-            at += n;
+            at += s.n;
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) static_cast<WsHeader*>(a.ws)->clusters = n_runs;
     tc::tc_fence_before();
     __syncthreads();
     tc::cluster_sync_all();                      // both CTAs' barriers and TMEM exist
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
@@ -361,8 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     if (warp == kPlanWarp<FP8>) {
         // ---------------- plan: the run's segments, then the units that hold padding only
         if (busy) {
-            int seg = 0, u = sm.u0, k0 = sm.k0;
-            long long left = hi - lo;
+            int seg = 1, u = sm.seg[0].unit + 1; // the first is out
+            long long left = hi - lo - (sm.seg[0].k1 - sm.seg[0].k0);
             bool ok = true;
             while (ok && left > 0) {
                 // 32 units at a time.
@@ -375,10 +388,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     s.seq = __shfl_sync(0xffffffffu, seq, i);
                     s.n = (s.len + kTile - 1) / kTile;
                     if (s.n == 0) continue;
-                    s.k0 = k0;
-                    s.k1 = (int)min((long long)s.n, s.k0 + left);
-                    k0 = 0;
-                    left -= s.k1 - s.k0;
+                    s.k0 = 0;
+                    s.k1 = (int)min((long long)s.n, left);
+                    left -= s.k1;
                     const int d = seg % kSegs;
                     ok = __all_sync(0xffffffffu, wait(&sm.seg_empty[d], ((seg / kSegs) + 1) & 1, abort_flag));
                     if (!ok) break;
@@ -587,34 +599,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
                 const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
                 const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
-                const bool f32 = !whole || a.o_f32, write = grow < k.group_rows;
-                const size_t orow = (size_t)g * k.group_rows + grow, srow = (size_t)slot * kM + rank * kRows + row;
-                uint8_t* ws = static_cast<uint8_t*>(a.ws);
-                float* of = whole ? static_cast<float*>(a.o) + orow * kDv : reinterpret_cast<float*>(ws + kWsO) + srow * kDv;
-                uint16_t* ob = static_cast<uint16_t*>(a.o) + orow * kDv;
+                const bool write = grow < k.group_rows;
+                const size_t orow = (size_t)g * k.group_rows + grow;
+                float4* part = part_o(a.ws, slot, rank) + L;
                 if (hf == 0 && wg == 0 && write) {
-                    if (!whole) reinterpret_cast<float*>(ws + kWsLse)[srow] = lse;
+                    if (!whole) part_lse(a.ws, slot)[rank * kRows + row] = lse;
                     else if (a.lse) a.lse[orow] = lse;
                 }
+                uint8_t* stage = sm.p[wg] + quarter * 2048;        // its product is done
 #pragma unroll 1
                 for (int c = wg * 128; c < wg * 128 + 128; c += 32) {
                     uint32_t ov[32];
                     tc::tmem_ld32(tmem + c + lane_off, ov);
                     tc::tmem_wait_ld();
-                    if (write) {
-                        float f[32];
+                    float f[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
-                        if (f32) {
-                            float4* d = reinterpret_cast<float4*>(of + hf * 256 + c);
+                    for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                    if (!whole) {                // lanes side by side
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) part[(c / 4 + e) * 128] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else if (a.o_f32) {
+                        float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + hf * 256 + c);
+                        if (write)
 #pragma unroll
                             for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                        } else {
-                            uint4* d = reinterpret_cast<uint4*>(ob + hf * 256 + c);
+                    } else {                     // 64 bytes of 32 rows through shared memory: 8 rows a store
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                d[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                                  pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) =
+                                make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                           pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int rr = e * 8 + lane / 4, ch = lane & 3;
+                            if (grow - row + (rr + quarter * 32 & 63) < k.group_rows)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + (orow - row + (rr + quarter * 32 & 63)) * kDv + hf * 256 + c + ch * 8) =
+                                    *reinterpret_cast<const uint4*>(stage + rr * 64 + ((ch ^ (rr >> 1 & 3)) << 4));
                         }
                     }
                     __syncwarp();
@@ -976,8 +997,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 }
 
 // Joins the partial results of the units that a run's start cuts.  Block (c, y): run c + 1's first unit, when that run
-// is the first to start inside it; warp = one of its rows.  Weights exp(lse - max), parts in key order.
-__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentKernelArgs k) {
+// is the first to start inside it; CTA rows y / 16, 16 dims of each half-row per thread (thread = lane of the partial
+// results).  Weights exp(lse - max), parts in key order.  Launched while the attention still runs: it waits for its end.
+__global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentKernelArgs k) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const LatentArgs& a = k.a;
     const WsHeader* w = static_cast<const WsHeader*>(a.ws);
     const int c = blockIdx.x + 1, n_runs = w->clusters;
@@ -986,28 +1009,25 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant
     if (w->unit[c - 1] == u && w->k0[c - 1] > 0) return;           // an earlier run is the first
     int last = c;
     while (last + 1 < n_runs && w->unit[last + 1] == u) ++last;    // every later run of the unit starts inside it
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int g = u / k.m_tiles, grow = (u - g * k.m_tiles) * kM + row;
+    const int rank = blockIdx.y >> 4, c4 = (blockIdx.y & 15) * 4, L = threadIdx.x, row = L & 63;
+    const int g = u / k.m_tiles, grow = (u - g * k.m_tiles) * kM + rank * kRows + row;
     if (grow >= k.group_rows) return;
-    const float* lses = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kWsLse) + row;
-    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kWsO) + (size_t)row * kDv;
     auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
     const int n = last - c + 2;
     float m = kNegInf;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, lses[slot(i) * kM]);
-    m = warp_max(m);
+    for (int i = 0; i < n; ++i) m = fmaxf(m, part_lse(a.ws, slot(i))[rank * kRows + row]);
     float acc[16], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        const float lse = lses[slot(i) * kM];
-        if (lse == kNegInf) continue;
-        const float wt = expf(lse - m);
+        const float lse = part_lse(a.ws, slot(i))[rank * kRows + row];
+        const float wt = lse == kNegInf ? 0.f : expf(lse - m);     // a part without keys holds zeros
+        const float4* p = part_o(a.ws, slot(i), rank) + (size_t)c4 * 128 + L;
         sum += wt;
-        const float4* p = reinterpret_cast<const float4*>(parts + (size_t)slot(i) * kM * kDv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float4 v = p[e * 32 + lane];
+            const float4 v = p[e * 128];
             acc[4 * e] = fmaf(wt, v.x, acc[4 * e]);
             acc[4 * e + 1] = fmaf(wt, v.y, acc[4 * e + 1]);
             acc[4 * e + 2] = fmaf(wt, v.z, acc[4 * e + 2]);
@@ -1015,15 +1035,21 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const size_t orow = (size_t)g * k.group_rows + grow;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float4 v = make_float4(acc[4 * e] * inv, acc[4 * e + 1] * inv, acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
-        if (a.o_f32) reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv)[e * 32 + lane] = v;
-        else reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + orow * kDv)[e * 32 + lane] =
-                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    for (int e = 0; e < 16; ++e) acc[e] *= inv;
+    const size_t orow = (size_t)g * k.group_rows + grow, at = orow * kDv + (L >> 6) * 256 + c4 * 4;
+    if (a.o_f32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            reinterpret_cast<float4*>(static_cast<float*>(a.o) + at)[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at)[e] =
+                make_uint4(pack_bf16x2(acc[8 * e], acc[8 * e + 1]), pack_bf16x2(acc[8 * e + 2], acc[8 * e + 3]),
+                           pack_bf16x2(acc[8 * e + 4], acc[8 * e + 5]), pack_bf16x2(acc[8 * e + 6], acc[8 * e + 7]));
     }
-    if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
+    if (L < kRows && c4 == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
 }
 
 // The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x 8 x `chunks` x 1; BF16 under the 128-byte swizzle, codes plain.
@@ -1082,8 +1108,17 @@ cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtenso
     latent_attn_kernel<FP8><<<2 * k.clusters, kThreadsOf<FP8>, smem, st>>>(qm, km, xm, k);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || k.clusters == 1) return e;
-    latent_merge_kernel<<<dim3(k.clusters - 1, kM / 8), 256, 0, st>>>(k);
-    return cudaGetLastError();
+    // The join is launched while the attention runs, and waits for its end on the device.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(k.clusters - 1, 32);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel, k);
 }
 
 }  // namespace
