@@ -2,11 +2,13 @@
 //
 // (u, w) -> mscale (u cos a - w sin a, w cos a + u sin a) per pair of dimensions, a = position * frequency;
 // the gradient is the rotation by -a.  One read and one write of every element, 3 multiply-adds a pair:
-// bound by memory, so the split serves loads in flight.  A block takes one run of (token, head) rows of a
-// few tokens; its sines and cosines (one per token and pair, whatever the number of heads) are made once in
-// shared memory while the first loads travel.  A work item is 16 bytes of dimensions that are only copied,
-// or the 16 (interleaved) or 2 x 16 bytes (half layout) of whole pairs; kBatch items are loaded per thread
-// before any is used.
+// bound by memory, so the split keeps loads in flight and indexing cheap.  A block takes a run of (token, head) rows,
+// first the dimensions that are only copied, then the rotary ones, so that no warp mixes the two (mixed, every warp
+// paid for the rotation: 104 us instead of 54 for 8192 tokens x 64 heads of 128, half rotated).  A thread keeps one
+// item of the row -- 16 bytes to copy, or the 16 (interleaved) or 2 x 16 bytes (half layout) of whole pairs -- and walks
+// down the rows, several of them loaded before any is used.  The sines and cosines (one per token and pair, whatever
+// the number of heads) are made once in shared memory, before the copies, and stay in registers from one head to the
+// next.
 #include <cmath>
 
 #include "kernels.cuh"
@@ -17,7 +19,7 @@ namespace lsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kBatch = 4;                        // items in flight per thread
+constexpr int kCopyBatch = 4, kRotBatch = 2;     // rows in flight per thread
 constexpr int kMaxTokens = 16;                   // tokens of a block (their table in shared memory)
 
 struct RopeArgs {
@@ -41,109 +43,131 @@ __device__ __forceinline__ void from_f(float& d, float v) { d = v; }
 template <typename T, int E>
 struct alignas(sizeof(T) * E) Pack { T v[E]; };
 
-// An item's loaded elements: `a` from dimension d0, and `b` its partners (rotary items, half layout: from d0 + rd / 2).
-template <typename T, int E>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
-    extern __shared__ float2 cs[];               // [tokens][rd / 2]
-    using P = Pack<T, E>;
-    const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
-    const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
-    const int rd = p.r.rot_dim, half = rd / 2;
-    const bool inter = p.r.interleaved;
-    // A row's items: the rotary ones first, then the copied runs before and behind the rotary dimensions.
-    // Scalars (E = 1): a pair per rotary item, one element per copied item.
-    const int n_rot = inter ? (E > 1 ? rd / E : half) : half / E;
-    const int n_row = n_rot + (p.copy ? (p.D - rd) / E : 0);
-    const int n = nt * nh * n_row;
-    const T* x = static_cast<const T*>(p.x);
-    T* y = static_cast<T*>(p.y);
-    bool ready = false;
-    for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < n; i0 += kRopeThreads * kBatch) {
-        P a[kBatch], b[kBatch];
-        int64_t ya[kBatch];
-        int rot[kBatch];                         // table index of the item's first pair, or -1
+// Rotary items of a row.  Scalars (E = 1): a pair per item.
+template <int E, bool INTER>
+__host__ __device__ inline int rot_items(int rd) { return INTER && E > 1 ? rd / E : rd / 2 / E; }
+
+// Walks the rows of a block (nh heads of each token) with `n` items each: item(c) is called for each item column of this
+// thread, then rows(tokens, heads, count) for BATCH rows at a time, count of them live.
+template <int BATCH, typename Item, typename Rows>
+__device__ __forceinline__ void walk(int n, int rows, int nh, Item item, Rows body) {
+    const int cols = min(n, kRopeThreads), step = kRopeThreads / cols;             // items and rows of a pass
+    const int r0 = threadIdx.x / cols, dt = step / nh, dh = step - dt * nh;
+    if (r0 >= step) return;
+    for (int c = threadIdx.x - r0 * cols; c < n; c += cols) {
+        item(c);
+        int t = r0 / nh, h = r0 - t * nh;
+        for (int row = r0; row < rows; row += step * BATCH) {
+            int tt[BATCH], hh[BATCH];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int i = i0 + u * kRopeThreads;
-            rot[u] = -2;
-            if (i >= n) continue;
-            const int row = i / n_row, it = i - row * n_row;
-            const int tl = row / nh, h = h0 + row - tl * nh, t = t0 + tl;
-            const int64_t xa = t * p.xt + h * p.xh;
-            int d;
-            if (it < n_rot) {
-                const int pair = inter ? it * (E > 1 ? E / 2 : 1) : it * E;
-                rot[u] = tl * half + pair;
-                d = p.off + (inter ? 2 * pair : pair);
-                if (!inter) b[u] = *reinterpret_cast<const P*>(x + xa + d + half);
-                else if (E == 1) b[u] = *reinterpret_cast<const P*>(x + xa + d + 1);
-            } else {
-                rot[u] = -1;
-                d = (it - n_rot) * E;
-                if (d >= p.off) d += rd;
+            for (int u = 0; u < BATCH; ++u) {
+                tt[u] = t;
+                hh[u] = h;
+                t += dt;
+                h += dh;
+                if (h >= nh) { h -= nh; ++t; }
             }
-            a[u] = *reinterpret_cast<const P*>(x + xa + d);
-            ya[u] = t * p.yt + h * p.yh + d;
-        }
-        if (!ready) {                            // the table, once, under the first loads
-            for (int k = threadIdx.x; k < nt * half; k += kRopeThreads) {
-                const int tl = k / half, i = k - tl * half;
-                float2 v = rope_cs(p.pos[t0 + tl], p.r.rev_freq[i], p.r.mscale);
-                v.y *= p.sign;
-                cs[k] = v;
-            }
-            __syncthreads();
-            ready = true;
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (rot[u] == -2) continue;
-            if (rot[u] >= 0) {
-                if (inter && E > 1) {
-#pragma unroll
-                    for (int e = 0; e + 1 < E; e += 2) {
-                        const float2 c = cs[rot[u] + e / 2];
-                        const float f = to_f(a[u].v[e]), g = to_f(a[u].v[e + 1]);
-                        from_f(a[u].v[e], f * c.x - g * c.y);
-                        from_f(a[u].v[e + 1], g * c.x + f * c.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float2 c = cs[rot[u] + e];
-                        const float f = to_f(a[u].v[e]), g = to_f(b[u].v[e]);
-                        from_f(a[u].v[e], f * c.x - g * c.y);
-                        from_f(b[u].v[e], g * c.x + f * c.y);
-                    }
-                    *reinterpret_cast<P*>(y + ya[u] + (inter ? 1 : half)) = b[u];
-                }
-            }
-            *reinterpret_cast<P*>(y + ya[u]) = a[u];
+            body(tt, hh, (rows - row + step - 1) / step);
         }
     }
 }
 
-template <typename T, int E>
-cudaError_t launch_rope_t(RopeArgs& p, cudaStream_t st) {
-    // Tokens per block so that a block has about two rounds of items (32 KB), heads per block so that the
-    // grid covers the GPU: few tokens split their heads, many tokens with few heads share a block.
-    const int n_row = (p.r.interleaved ? (E > 1 ? p.r.rot_dim / E : p.r.rot_dim / 2) : p.r.rot_dim / 2 / E) +
-                      (p.copy ? (p.D - p.r.rot_dim) / E : 0);
-    const int want = 2 * kBatch * kRopeThreads;
+template <typename T, int E, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
+    extern __shared__ float2 cs[];               // [tokens][rd / 2]
+    using P = Pack<T, E>;
+    constexpr bool kIn = INTER && E > 1;         // both of a pair in the same pack
+    constexpr int kPairs = kIn ? E / 2 : E;      // pairs of a rotary item
+    const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
+    const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
+    const int rd = p.r.rot_dim, half = rd / 2;
+    const T* x = static_cast<const T*>(p.x) + t0 * p.xt + h0 * p.xh;
+    T* y = static_cast<T*>(p.y) + t0 * p.yt + h0 * p.yh;
+    for (int k = threadIdx.x; k < nt * half; k += kRopeThreads) {
+        const int t = k / half, i = k - t * half;
+        float2 v = rope_cs(p.pos[t0 + t], p.r.rev_freq[i], p.r.mscale);
+        v.y *= p.sign;
+        cs[k] = v;
+    }
+    if (p.copy && p.D > rd) {
+        int d = 0;
+        walk<kCopyBatch>((p.D - rd) / E, nt * nh, nh, [&](int c) { d = c * E < p.off ? c * E : c * E + rd; },
+            [&](const int* tt, const int* hh, int n) {
+                P a[kCopyBatch];
+#pragma unroll
+                for (int u = 0; u < kCopyBatch; ++u)
+                    if (u < n) a[u] = *reinterpret_cast<const P*>(x + tt[u] * p.xt + hh[u] * p.xh + d);
+#pragma unroll
+                for (int u = 0; u < kCopyBatch; ++u)
+                    if (u < n) *reinterpret_cast<P*>(y + tt[u] * p.yt + hh[u] * p.yh + d) = a[u];
+            });
+    }
+    __syncthreads();
+    const int d2 = INTER ? 1 : half;             // where an item's partners are (interleaved packs hold both)
+    int d = 0, pair = 0, have = -1;
+    float2 c[kPairs];
+    walk<kRotBatch>(rot_items<E, INTER>(rd), nt * nh, nh,
+        [&](int it) {
+            pair = it * kPairs;
+            d = p.off + (INTER ? 2 * pair : pair);
+            have = -1;
+        },
+        [&](const int* tt, const int* hh, int n) {
+            P a[kRotBatch], b[kRotBatch];
+#pragma unroll
+            for (int u = 0; u < kRotBatch; ++u)
+                if (u < n) {
+                    const T* s = x + tt[u] * p.xt + hh[u] * p.xh + d;
+                    a[u] = *reinterpret_cast<const P*>(s);
+                    if (!kIn) b[u] = *reinterpret_cast<const P*>(s + d2);
+                }
+#pragma unroll
+            for (int u = 0; u < kRotBatch; ++u)
+                if (u < n) {
+                    if (tt[u] != have) {
+                        have = tt[u];
+#pragma unroll
+                        for (int e = 0; e < kPairs; ++e) c[e] = cs[have * half + pair + e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        T& fu = a[u].v[kIn ? 2 * e : e];
+                        T& gu = kIn ? a[u].v[2 * e + (kIn ? 1 : 0)] : b[u].v[e];
+                        const float f = to_f(fu), g = to_f(gu);
+                        from_f(fu, f * c[e].x - g * c[e].y);
+                        from_f(gu, g * c[e].x + f * c[e].y);
+                    }
+                    T* o = y + tt[u] * p.yt + hh[u] * p.yh + d;
+                    *reinterpret_cast<P*>(o) = a[u];
+                    if (!kIn) *reinterpret_cast<P*>(o + d2) = b[u];
+                }
+        });
+}
+
+template <typename T, int E, bool INTER>
+cudaError_t launch_rope_i(RopeArgs& p, cudaStream_t st) {
+    // Rows per block: about 16 items a thread, so that a block's start (its table) is a small part of it; fewer when the
+    // grid would not cover the 148 SMs a few times.
+    const int n_row = rot_items<E, INTER>(p.r.rot_dim) + (p.copy ? (p.D - p.r.rot_dim) / E : 0);
+    const int64_t want = 16 * kRopeThreads;
     p.heads = p.H;
     p.tokens = 1;
-    if ((int64_t)p.H * n_row > want) p.heads = (want + n_row - 1) / n_row;
+    if ((int64_t)p.H * n_row > want) p.heads = (int)((want + n_row - 1) / n_row);
     else while (p.tokens < kMaxTokens && (int64_t)2 * p.tokens * p.H * n_row <= want) p.tokens *= 2;
-    // Too few blocks for 148 SMs: smaller ones, down to one round of items each.
     auto blocks = [&] { return (int64_t)((p.T + p.tokens - 1) / p.tokens) * ((p.H + p.heads - 1) / p.heads); };
-    while (blocks() < 2 * 148 && (int64_t)p.tokens * p.heads * n_row > kRopeThreads) {
+    while (blocks() < 4 * 148 && (int64_t)p.tokens * p.heads * n_row > kRopeThreads) {
         if (p.tokens > 1) p.tokens /= 2;
         else if (p.heads > 1) p.heads = (p.heads + 1) / 2;
         else break;
     }
     dim3 grid((p.T + p.tokens - 1) / p.tokens, (p.H + p.heads - 1) / p.heads);
-    rope_kernel<T, E><<<grid, kRopeThreads, (size_t)p.tokens * p.r.rot_dim / 2 * sizeof(float2), st>>>(p);
+    rope_kernel<T, E, INTER><<<grid, kRopeThreads, (size_t)p.tokens * p.r.rot_dim / 2 * sizeof(float2), st>>>(p);
     return cudaGetLastError();
+}
+
+template <typename T, int E>
+cudaError_t launch_rope_t(RopeArgs& p, cudaStream_t st) {
+    return p.r.interleaved ? launch_rope_i<T, E, true>(p, st) : launch_rope_i<T, E, false>(p, st);
 }
 
 }  // namespace
