@@ -56,6 +56,7 @@ constexpr int kQTmem = 6;                                        // query atoms 
 constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
 constexpr int kMaxClusters = 80;
+constexpr int kMinRun = 2;                       // key tiles of a run at least: a shorter one costs more to join than it saves
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8;
 // The other warps.  FP8 (24 warps): the widening warps keep off the scheduler of the MMA warp (warp mod 4 = 0).
 template <bool FP8> constexpr int kPlanWarp = FP8 ? 20 : 9;
@@ -222,7 +223,9 @@ __device__ __noinline__ int page_of(const LatentArgs& a, int seq, int row, int* 
 __device__ __noinline__ int unit_len(const LatentKernelArgs& k, int u, int* seq, bool tell) {
     const LatentArgs& a = k.a;
     const int g = u / k.m_tiles, r0 = (u - g * k.m_tiles) * kM, r1 = min(k.group_rows, r0 + kM);
-    const int t0 = g * a.q_group, b = a.q_seq[t0];
+    const int t0 = g * a.q_group, ta = t0 + r0 / a.H, tb = t0 + (r1 - 1) / a.H;
+    const int b = a.q_seq[t0];
+    int pos = a.q_pos[ta], sq = a.q_seq[ta];     // asked for before the sequence's length is
     int sl = 0;
     if (b >= 0 && b < a.B) {
         sl = a.seq_len[b];
@@ -231,11 +234,12 @@ __device__ __noinline__ int unit_len(const LatentKernelArgs& k, int u, int* seq,
     *seq = b;
     int len = 0;
     bool bad = false;
-    for (int t = t0 + r0 / a.H; t <= t0 + (r1 - 1) / a.H; ++t) {
-        const int pos = a.q_pos[t];
-        if (pos < 0) continue;
-        if (pos < sl && a.q_seq[t] == b) len = max(len, pos + 1);
-        else bad = true;
+    for (int t = ta;; pos = a.q_pos[t], sq = a.q_seq[t]) {
+        if (pos >= 0) {
+            if (pos < sl && sq == b) len = max(len, pos + 1);
+            else bad = true;
+        }
+        if (++t > tb) break;
     }
     if (bad && tell) report(a.status, LSA_ERR_DEVICE_DATA);
     return len;
@@ -289,14 +293,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         tc::fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc2(&sm.tmem_base, 512);
+    if (threadIdx.x == 32) {
+        tc::prefetch_tmap(&qmap);
+        tc::prefetch_tmap(&kmap);
+        tc::prefetch_tmap(&xmap);
+    }
 
     // The plan: tiles per unit, summed over the block; each thread takes a run of units.
     const int per = (k.units + kThreads - 1) / kThreads;
     const int ua = min(k.units, (int)threadIdx.x * per), ub = min(k.units, ua + per);
     long long mine = 0;
+    int len0 = 0, seq0 = 0;                      // of the thread's last unit
     for (int u = ua; u < ub; ++u) {
-        int seq;
-        mine += (unit_len(k, u, &seq, blockIdx.x == 0) + kTile - 1) / kTile;
+        len0 = unit_len(k, u, &seq0, blockIdx.x == 0);
+        mine += (len0 + kTile - 1) / kTile;
     }
     long long before = mine;
 #pragma unroll
@@ -312,14 +322,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         total += sm.scan[w];
     }
     before -= mine;
-    const int n_runs = (int)min((long long)k.clusters, total);
+    const int n_runs = (int)min((long long)k.clusters, (total + kMinRun - 1) / kMinRun);
     const long long lo = n_runs ? total * cluster / n_runs : 0, hi = n_runs ? total * (cluster + 1) / n_runs : 0;
     const bool busy = cluster < n_runs;
     if (busy && before <= lo && lo < before + mine) {              // one thread: the run starts among its units
         long long at = before;
         for (int u = ua; u < ub; ++u) {
             Seg s;
-            s.len = unit_len(k, u, &s.seq, false);
+            if (u == ub - 1) { s.len = len0; s.seq = seq0; }
+            else s.len = unit_len(k, u, &s.seq, false);
             s.n = (s.len + kTile - 1) / kTile;
             if (lo < at + s.n) {                 // and publishes the first segment at once
                 s.unit = u;
@@ -570,8 +581,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             if (have) {
                 const int g1 = s.unit / k.m_tiles, row1 = (s.unit - g1 * k.m_tiles) * kM + rank * kRows + row;
                 if (row1 < k.group_rows) {
-                    const int t = g1 * a.q_group + row1 / a.H, pos = a.q_pos[t];
-                    if (pos >= 0 && a.q_seq[t] == s.seq && pos < a.seq_len[s.seq]) lim = pos + 1;
+                    const int t = g1 * a.q_group + row1 / a.H;
+                    const int pos = a.q_pos[t], seq = a.q_seq[t], sl = a.seq_len[s.seq];        // together, then compared
+                    lim = pos >= 0 && seq == s.seq && pos < sl ? pos + 1 : 0;
                 }
             }
             if (!first) {
@@ -1002,8 +1014,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentKernelArgs k) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const LatentArgs& a = k.a;
-    const WsHeader* w = static_cast<const WsHeader*>(a.ws);
-    const int c = blockIdx.x + 1, n_runs = w->clusters;
+    const WsHeader* ws = static_cast<const WsHeader*>(a.ws);
+    __shared__ WsHeader sh;                      // read at once: the runs of a unit are counted one after another
+    WsHeader* w = &sh;
+    for (int i = threadIdx.x; i < kMaxClusters; i += blockDim.x) { w->unit[i] = ws->unit[i]; w->k0[i] = ws->k0[i]; }
+    const int c = blockIdx.x + 1, n_runs = ws->clusters;
+    __syncthreads();
     if (c >= n_runs || w->k0[c] == 0) return;
     const int u = w->unit[c];
     if (w->unit[c - 1] == u && w->k0[c - 1] > 0) return;           // an earlier run is the first
@@ -1015,11 +1031,12 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant
     auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
     const int n = last - c + 2;
     float m = kNegInf;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) m = fmaxf(m, part_lse(a.ws, slot(i))[rank * kRows + row]);
     float acc[16], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < n; ++i) {
         const float lse = part_lse(a.ws, slot(i))[rank * kRows + row];
         const float wt = lse == kNegInf ? 0.f : expf(lse - m);     // a part without keys holds zeros
@@ -1105,6 +1122,9 @@ cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtenso
     const size_t smem = sizeof(Smem) + 1024;
     k.clusters = cluster_count<FP8>(smem);
     if (k.clusters < 1) return cudaErrorInvalidConfiguration;
+    // No more clusters than the allocated rows can need: a short context launches few, and one alone has nothing to join.
+    const int64_t tiles = (int64_t)k.units * ((k.a.L_alloc + kTile - 1) / kTile);
+    if ((tiles + kMinRun - 1) / kMinRun < k.clusters) k.clusters = (int)((tiles + kMinRun - 1) / kMinRun);
     latent_attn_kernel<FP8><<<2 * k.clusters, kThreadsOf<FP8>, smem, st>>>(qm, km, xm, k);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || k.clusters == 1) return e;
