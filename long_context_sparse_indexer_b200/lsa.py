@@ -389,8 +389,8 @@ def _stream_on(dev: int, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _float_vec(t: Optional[torch.Tensor], n: int, name: str) -> None:
-    if t is not None and (t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous()):
+def _float_vec(t: torch.Tensor, n: int, name: str) -> None:
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous float32 tensor of {n} elements")
 
 
@@ -436,35 +436,38 @@ class PageTable:
     [pages, page rows, dim], and position p of sequence b is row p % page rows of page table[b, p // page rows]."""
     table: torch.Tensor
 
-    def c(self, cache: Cache) -> CPages:
-        t = self.table
-        if t.dim() != 2 or t.dtype is not torch.int32 or t.stride(1) != 1:
-            raise ValueError("page table: int32 [sequences, pages per sequence] with contiguous rows")
-        B, n = t.shape
-        return CPages(t.data_ptr(), t.stride(0) if B > 1 else n, n, cache.data.shape[1], cache.data.shape[0], 0)
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _cache_c(cache: Cache, pages: Optional[PageTable], B: int, rows: int):
     """The C cache and page table (None: a cache of the batch's B sequences of at least `rows` rows), checked."""
     d, sc = cache.data, cache.scale
-    if d.dim() != 3 or d.stride(2) != 1:
-        raise ValueError("cache: [sequences or pages, rows, dim] with contiguous rows")
+    if d.dim() != 3:
+        raise ValueError("cache: [sequences or pages, rows, dim]")
     n, r, dim = d.shape
-    dt = cache.dtype
-    sss = 0
-    if dt == FP8_E4M3:
-        if sc is None or sc.dtype is not torch.float32 or sc.shape != d.shape[:2] or sc.stride(1) != 1:
+    s0, s1, s2 = d.stride()
+    if s2 != 1:
+        raise ValueError("cache: rows of contiguous elements")
+    if d.dtype is torch.bfloat16:
+        cc = CCache(d.data_ptr(), None, BF16, dim, s0, s1, 0)
+    elif d.dtype in _E4M3:
+        if sc is None or sc.dtype is not torch.float32 or sc.dim() != 2 or sc.size(0) != n or sc.size(1) != r or sc.stride(1) != 1:
             raise ValueError("cache scale: float32 [sequences or pages, rows] with contiguous rows")
-        sss = sc.stride(0)
-    cc = CCache(d.data_ptr(), sc.data_ptr() if sss else None, dt, dim, d.stride(0), d.stride(1), sss)
+        cc = CCache(d.data_ptr(), sc.data_ptr(), FP8_E4M3, dim, s0, s1, sc.stride(0))
+    else:
+        raise ValueError(f"unsupported cache dtype {d.dtype}")
     if pages is None:
         if n < B or r < rows:
             raise ValueError("cache: fewer sequences or rows than the batch")
         return cc, None
-    cp = pages.c(cache)
-    if pages.table.shape[0] < B:
+    t = pages.table
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.stride(1) != 1:
+        raise ValueError("page table: int32 [sequences, pages per sequence] with contiguous rows")
+    tb, tn = t.shape
+    if tb < B:
         raise ValueError("page table: fewer sequences than the batch")
-    return cc, cp
+    return cc, CPages(t.data_ptr(), t.stride(0) if tb > 1 else tn, tn, r, n, 0)
 
 
 def rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: Optional[torch.Tensor] = None, offset: int = 0,
@@ -504,12 +507,14 @@ def cache_append(batch: Batch, x: torch.Tensor, cache: Cache, pages: Optional[Pa
     elements, default all), rotated (rope, at rope_offset) and stored at each token's position of the cache."""
     if norm not in _NORMS:
         raise ValueError(f"unknown norm {norm!r}")
-    T, dim = batch.q_seq.numel(), cache.data.shape[-1]
-    if x.dim() != 2 or x.shape != (T, dim) or x.dtype is not torch.bfloat16 or x.stride(1) != 1:
+    T, dim = batch.q_seq.numel(), cache.data.size(-1)
+    if x.dim() != 2 or x.size(0) != T or x.size(1) != dim or x.dtype is not torch.bfloat16 or x.stride(1) != 1:
         raise ValueError("cache_append: x is [T, dim] bf16 with contiguous rows")
-    norm_dim = int(norm_dim or dim)
-    _float_vec(gamma, norm_dim, "gamma")
-    _float_vec(beta, norm_dim, "beta")
+    norm_dim = norm_dim or dim
+    if gamma is not None:
+        _float_vec(gamma, norm_dim, "gamma")
+    if beta is not None:
+        _float_vec(beta, norm_dim, "beta")
     cb = _batch_c(batch, T)
     cc, cp = _cache_c(cache, pages, cb.B, batch.L_alloc)
     dev = _launch_device(x, cache.data, cache.scale, gamma, beta, dev_status, batch.q_pos, batch.q_seq, batch.seq_len,
@@ -536,11 +541,12 @@ def latent_attn(batch: Batch, q: torch.Tensor, cache: Cache, sm_scale: float, o:
     """lsa_latent_attn: q [T, H, 576] bf16 over every cached row up to each token's position -> o [T, H, 512]
     (bf16, or float32 for a later merge_partials), lse [T, H] float32.  ws: latent_attn_workspace_size bytes."""
     T = batch.q_seq.numel()
-    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != 576 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+    if q.dim() != 3 or q.size(0) != T or q.size(2) != 576 or q.dtype is not torch.bfloat16 or not q.is_contiguous():
         raise ValueError("latent_attn: q is contiguous bf16 [T, H, 576]")
-    H = q.shape[1]
+    H = q.size(1)
     dt = _out_dtype(o, (T, H, 512))
-    _float_vec(lse, T * H, "lse")
+    if lse is not None:
+        _float_vec(lse, T * H, "lse")
     cb = _batch_c(batch, T)
     cc, cp = _cache_c(cache, pages, cb.B, batch.L_alloc)
     dev = _launch_device(q, o, lse, ws, dev_status, cache.data, cache.scale, batch.q_pos, batch.q_seq, batch.seq_len,
@@ -568,7 +574,8 @@ def latent_attn_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Te
     if q.dtype is not bf or k_nope.dtype is not bf or k_rope.dtype is not bf or v.dtype is not bf or not qd == kd == rd == vd == 1:
         raise ValueError("latent_attn_expanded: bf16 inputs with a contiguous last dimension")
     dt = _out_dtype(o, (T, H, 128))
-    _float_vec(lse, T * H, "lse")
+    if lse is not None:
+        _float_vec(lse, T * H, "lse")
     B = q_start.numel() - 1
     _int_vec(q_start, B + 1, "q_start")
     _int_vec(k_start, B + 1, "k_start")
