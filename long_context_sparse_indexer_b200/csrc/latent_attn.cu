@@ -27,8 +27,9 @@
 //
 // Warps: 0..3 and 4..7 softmax, alternate tiles (thread = TMEM lane = (row, half of the keys); the two halves of a row
 // exchange their maxima through shared memory), 8 the MMAs (in CTA 0, for both), 9 the plan of the cluster's segments.
-// BF16: 10 and 11 load keys and exchanged rows by TMA.  FP8: 10 loads a tile's codes into the head of the stage that
-// they widen into, 11..18 widen them there and 19..22 the exchanged rows (bit moves only), 23 brings the row scales.
+// BF16: 10 and 11 load keys and exchanged rows by TMA.  FP8: 16 loads a tile's codes into the tail of the stage that they
+// widen into (bit moves only), eight warps widen them there and four the exchanged rows, one brings the row scales, and
+// the plan is 21's.
 // All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
 #include <cmath>
 #include <cstring>
@@ -58,8 +59,8 @@ constexpr int kSegs = 3;                                         // published se
 constexpr int kMaxClusters = 80;
 constexpr int kMinRun = 2;                       // key tiles of a run at least: a shorter one costs more to join than it saves
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8;
-// The other warps.  FP8 (24 warps): the widening warps keep off the scheduler of the MMA warp (warp mod 4 = 0).
-template <bool FP8> constexpr int kPlanWarp = FP8 ? 20 : 9;
+// The other warps.  FP8 (24 warps): the four schedulers (warp mod 4) share the widening evenly, the MMAs' with less of it.
+template <bool FP8> constexpr int kPlanWarp = FP8 ? 21 : 9;
 template <bool FP8> constexpr int kLoadWarp = FP8 ? 16 : 10;     // queries and own keys
 template <bool FP8> constexpr int kXWarp = FP8 ? -1 : 11;        // BF16: exchanged rows
 constexpr int kKWarps = 8, kXWarps = 4;                          // FP8 converters
@@ -865,9 +866,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     } else if (busy && FP8) {
         // ---------------- FP8.  Eight warps widen the own keys' codes landed in the stage, four the exchanged rows', one brings
         // the row scales.
-        // Warps 9, 13, 17, 21 and 10, 14, 18, 22: own keys; 11, 15, 19, 23: exchanged rows.
-        const int role = warp & 3, nth = (warp - 8) >> 2;
-        const int w = role == 0 ? kKWarps + kXWarps : (role - 1) * 4 + nth;
+        // Own keys 0..7: warps 9, 10, 11, 12 and 13, 14, 15, 17; exchanged rows 8..11: 18, 19, 20, 23; scales 12: 22.
+        const int w = warp < 16 ? warp - 9 : (warp == 17 ? 7 : (warp == 22 ? 12 : (warp == 23 ? 11 : warp - 10)));
         int r = 0, tile = 0;
         uint32_t ph = 0;                         // parity of each stage's next phase (codes landed; scores done)
         bool ok = true;
@@ -876,8 +876,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         auto widen = [&](const uint8_t* from, uint8_t* to, int n) {
             uint8_t* to2 = reinterpret_cast<uint8_t*>((uintptr_t)to ^ 16);         // the next 8 dims under the swizzle
             uint4 next = *reinterpret_cast<const uint4*>(from);
-#pragma unroll 1                                 // a small loop: the roles share the instruction caches
-            for (int c = 0; c < n; ++c) {
+#pragma unroll 3                                 // the roles share the instruction caches: unrolled whole, 537 instead of 447 us
+            for (int c = 0; c < n; ++c) {        // for 32 tokens of 128 heads at 32K-64K
                 const uint4 v = next;
                 from += kAtom / 2;
                 if (c + 1 < n) next = *reinterpret_cast<const uint4*>(from);
