@@ -15,9 +15,15 @@
 // tile is five units, three K atoms (64 dims x 128 keys; two of k_nope, the rotary one) and two V units (64 keys
 // x 128 dims), each released as soon as its last product is issued.
 //
-// Warps: 0..3 softmax of query tile 0 (thread = row = TMEM lane), 4..7 of tile 1, 8 issues the MMAs, 9 the TMA
-// loads, 10 clears the rows of the last key tile that lie behind the sequence (0 x whatever they hold would
-// reach O).  All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
+// Items.  A CTA that runs takes over grid blocks that have not been launched yet (cluster launch control), so that the
+// start of one block's work -- its plan, queries and first scores -- runs under the end of another's; the order of the
+// grid, heaviest query tiles of a head first, stays.  The next block is asked for a few key tiles before the end of the
+// one in work, so that no CTA holds two while another has none.
+//
+// Warps: 0..3 softmax of query tile 0 (thread = row = TMEM lane), 4..7 of tile 1, 8 issues the MMAs, 9 loads keys and
+// values by TMA, 10 clears the rows of a sequence's last key tile that lie behind the sequence (0 x whatever they hold
+// would reach O), 11 takes the blocks, plans them and loads their queries.  All waits are bounded; a CTA that gives up
+// reports LSA_ERR_TIMEOUT.
 #include <cmath>
 #include <cstring>
 
@@ -36,22 +42,32 @@ constexpr int kPerTile = 5;                      // units of a key tile: K atoms
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split within the launch's registers");
 
+struct Item {
+    int q0, rows, k0, nk, shift;                 // first query row (packed), queries here, first key row, keys, nk - nq
+    int i0;                                      // index of the first query in its sequence
+    int n[2];                                    // key tiles of each query tile
+    int h;
+    int more;                                    // 0: no item, the end
+};
+
+constexpr int kItems = 2;                        // published items
+constexpr int kConsumers = 11;                   // warps that read them
+constexpr int kAskAhead = 6;                     // key tiles before an item's end at which the next block is asked for
+
 struct Smem {
     alignas(1024) uint8_t q[2][3][kM * 128];     // query tiles, 64-dim atoms
     alignas(1024) uint8_t ring[kUnits][kUnitBytes];
+    alignas(16) uint8_t answer[16];              // of the request for a block
+    Item item[kItems];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t asked, ask;                         // the answer is there; the loads are close to the item's end
     uint64_t full[kUnits], empty[kUnits];
-    uint64_t q_full;
+    uint64_t q_full, q_free;                     // the item's queries have landed; its last scores are done
     uint64_t v_last[2];                          // a partial last tile's V units: landed, not yet cleared behind the sequence
     uint64_t mma_done;                           // committed once, after the last MMA (the issuer's drain)
     uint64_t s_full[2], p_full[2][2], o_done[2]; // p_full[tile][keys 0..63 / 64..127]
     uint32_t tmem_base;
     int abort;
-};
-
-struct Plan {
-    int q0, rows, k0, nk, shift;                 // first query row (packed), queries here, first key row, keys, nk - nq
-    int i0;                                      // index of the first query in its sequence
-    int n[2];                                    // key tiles of each query tile
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -72,39 +88,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, b = blockIdx.z;
     volatile int* abort_flag = &sm.abort;
 
-    // The longest query tiles of a causal sequence first.
-    Plan p;
-    {
-        const int qs = a.q_start[b], qe = a.q_start[b + 1], ks = a.k_start[b], ke = a.k_start[b + 1];
-        const bool inside = qs >= 0 && qe >= qs && qe <= a.T && ks >= 0 && ke >= ks && ke <= a.S;
-        const int nq = inside ? qe - qs : 0;
-        if ((!inside || nq > a.max_q) && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) report(a.status, LSA_ERR_DEVICE_DATA);
-        const int todo = min(nq, a.max_q);
-        p.i0 = ((todo + 2 * kM - 1) / (2 * kM) - 1 - (int)blockIdx.x) * 2 * kM;
-        if (p.i0 < 0) return;                    // the whole CTA, before any barrier
-        p.q0 = qs + p.i0;
-        p.rows = min(2 * kM, todo - p.i0);
-        p.k0 = ks;
-        p.nk = ke - ks;
-        p.shift = p.nk - nq;
-        for (int t = 0; t < 2; ++t) {
-            const int r = min(kM, p.rows - t * kM);               // rows of the tile
-            const int end = r <= 0 ? 0 : (a.causal ? min(p.nk, max(0, p.i0 + t * kM + r + p.shift)) : p.nk);
-            p.n[t] = (end + kN - 1) / kN;
-        }
-    }
-    const int n_tiles = max(p.n[0], p.n[1]);
-    const bool partial = n_tiles * kN > p.nk;    // the last key tile reaches behind the sequence
-
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kItems; ++i) {
+            tc::mbar_init(&sm.item_full[i], 1);
+            tc::mbar_init(&sm.item_empty[i], kConsumers);
+        }
+        tc::mbar_init(&sm.asked, 1);
+        tc::mbar_init(&sm.ask, 1);
         for (int i = 0; i < kUnits; ++i) {
             tc::mbar_init(&sm.full[i], 1);
             tc::mbar_init(&sm.empty[i], 1);
         }
         tc::mbar_init(&sm.q_full, 1);
+        tc::mbar_init(&sm.q_free, 1);
         tc::mbar_init(&sm.v_last[0], 1);
         tc::mbar_init(&sm.v_last[1], 1);
         tc::mbar_init(&sm.mma_done, 1);
@@ -118,121 +116,250 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_barrier_init();
     }
     if (warp == 8) tc::tmem_alloc(&sm.tmem_base, 512);
+    if (threadIdx.x == 9 * 32) {
+        tc::prefetch_tmap(&qmap);
+        tc::prefetch_tmap(&kmap);
+        tc::prefetch_tmap(&rmap);
+        tc::prefetch_tmap(&vmap);
+    }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
+    // Items, as every role but warp 11 takes them.
+    int item_i = 0;
+    auto next_item = [&](Item& p) -> bool {
+        const int d = item_i % kItems;
+        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.item_full[d], (item_i / kItems) & 1, abort_flag));
+        p = sm.item[d];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.item_empty[d]);
+        ++item_i;
+        return ok && p.more;
+    };
+    auto tiles = [](const Item& p) { return max(p.n[0], p.n[1]); };
+    auto is_partial = [&](const Item& p) { return tiles(p) * kN > p.nk; };         // the last key tile reaches behind the sequence
+
     if (warp >= 8) {
         reg_dec<kOtherRegs>();
-        if (warp == 9) {
-            // ---------------- TMA loads: Q, then the ring's units in the order of their use
-            if (tc::elect_one() && n_tiles > 0) {
-                const int hq = a.qh ? h : 0, hk = a.kh ? h : 0, hv = a.vh ? h : 0;   // a broadcast head has no stride
-                const int n_q = p.rows > kM ? 2 : 1;
-                tc::mbar_expect_tx(&sm.q_full, n_q * 3 * kM * 128);
-                for (int t = 0; t < n_q; ++t)
-                    for (int c = 0; c < 3; ++c)
-                        tc::tma_load_3d(sm.q[t][c], &qmap, &sm.q_full, c * 64, hq, p.q0 + t * kM);
-                int u = 0, issued = 0;
-                for (int j = 0; j < n_tiles; ++j) {
-                    const int row = p.k0 + j * kN;
-                    bool ok = true;
-                    for (int c = 0; c < kPerTile; ++c, ++u) {
-                        const int s = u % kUnits;
-                        if (!tc::mbar_wait(&sm.empty[s], ((u / kUnits) + 1) & 1, abort_flag)) { ok = false; break; }
-                        // The V units of a partial last tile pass through warp 10, which then completes `full`.
-                        uint64_t* bar = c >= 3 && partial && j == n_tiles - 1 ? &sm.v_last[c - 3] : &sm.full[s];
-                        tc::mbar_expect_tx(bar, kUnitBytes);
-                        if (c < 2) tc::tma_load_3d(sm.ring[s], &kmap, bar, c * 64, hk, row);
-                        else if (c == 2) tc::tma_load_2d(sm.ring[s], &rmap, bar, 0, row);
-                        else {
-                            tc::tma_load_3d(sm.ring[s], &vmap, bar, 0, hv, row + (c - 3) * 64);
-                            tc::tma_load_3d(sm.ring[s] + 8192, &vmap, bar, 64, hv, row + (c - 3) * 64);
+        Item p;
+        if (warp == 11) {
+            // ---------------- blocks: the grid's own, then those not launched yet
+            if (tc::elect_one()) {
+                int x = blockIdx.x, h = blockIdx.y, b = blockIdx.z, published = 0, loaded = 0, asked = 0;
+                bool ok = true, more = true;
+                while (ok && more) {
+                    const int qs = a.q_start[b], qe = a.q_start[b + 1], ks = a.k_start[b], ke = a.k_start[b + 1];
+                    const bool inside = qs >= 0 && qe >= qs && qe <= a.T && ks >= 0 && ke >= ks && ke <= a.S;
+                    const int nq = inside ? qe - qs : 0, todo = min(nq, a.max_q);
+                    if ((!inside || nq > a.max_q) && x == 0 && h == 0) report(a.status, LSA_ERR_DEVICE_DATA);
+                    // The longest query tiles of a causal sequence first.
+                    p.i0 = ((todo + 2 * kM - 1) / (2 * kM) - 1 - x) * 2 * kM;
+                    if (p.i0 >= 0) {
+                        p.q0 = qs + p.i0;
+                        p.rows = min(2 * kM, todo - p.i0);
+                        p.k0 = ks;
+                        p.nk = ke - ks;
+                        p.shift = p.nk - nq;
+                        p.h = h;
+                        p.more = 1;
+                        for (int t = 0; t < 2; ++t) {
+                            const int r = min(kM, p.rows - t * kM);               // rows of the tile
+                            const int end = r <= 0 ? 0 : (a.causal ? min(p.nk, max(0, p.i0 + t * kM + r + p.shift)) : p.nk);
+                            p.n[t] = (end + kN - 1) / kN;
                         }
-                        issued = u + 1;
+                        const int d = published % kItems;
+                        ok = tc::mbar_wait(&sm.item_empty[d], ((published / kItems) + 1) & 1, abort_flag);
+                        if (!ok) break;
+                        sm.item[d] = p;
+                        tc::mbar_arrive(&sm.item_full[d]);
+                        ++published;
+                        if (tiles(p) > 0) {
+                            ok = loaded == 0 || tc::mbar_wait(&sm.q_free, (loaded - 1) & 1, abort_flag);
+                            if (!ok) break;
+                            const int hq = a.qh ? h : 0, n_q = p.rows > kM ? 2 : 1;        // a broadcast head has no stride
+                            tc::mbar_expect_tx(&sm.q_full, n_q * 3 * kM * 128);
+                            for (int t = 0; t < n_q; ++t)
+                                for (int c = 0; c < 3; ++c)
+                                    tc::tma_load_3d(sm.q[t][c], &qmap, &sm.q_full, c * 64, hq, p.q0 + t * kM);
+                            ok = tc::mbar_wait(&sm.ask, loaded & 1, abort_flag);
+                            ++loaded;
+                            if (!ok) break;
+                        }
                     }
+                    tc::fence_proxy_async_smem();            // the last answer has been read
+                    tc::mbar_expect_tx(&sm.asked, 16);
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                                 :: "r"(tc::smem_u32(sm.answer)), "r"(tc::smem_u32(&sm.asked)) : "memory");
+                    ok = tc::mbar_wait(&sm.asked, asked & 1, abort_flag);
+                    ++asked;
                     if (!ok) break;
+                    const volatile uint64_t* an = reinterpret_cast<const volatile uint64_t*>(sm.answer);
+                    uint32_t got, cx, cy, cz;
+                    asm volatile("{ .reg .b128 r; .reg .pred p; .reg .b32 w;\n"
+                                 "mov.b128 r, {%4, %5};\n"
+                                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+                                 "selp.u32 %0, 1, 0, p;\n"
+                                 "mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;\n"
+                                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, w}, r; }"
+                                 : "=r"(got), "=r"(cx), "=r"(cy), "=r"(cz) : "l"(an[0]), "l"(an[1]) : "memory");
+                    more = got != 0;
+                    x = (int)cx;
+                    h = (int)cy;
+                    b = (int)cz;
                 }
-                // No copy outlives the CTA: every unit issued has landed (at once unless a wait gave up).
+                if (ok) ok = tc::mbar_wait(&sm.item_empty[published % kItems], ((published / kItems) + 1) & 1, abort_flag);
+                if (ok) {
+                    sm.item[published % kItems].more = 0;
+                    tc::mbar_arrive(&sm.item_full[published % kItems]);
+                }
+                // No copy outlives the CTA.
                 volatile int drain = 0;
-                tc::mbar_wait(&sm.q_full, 0, &drain);
-                for (int v = max(0, issued - kUnits); v < issued; ++v) {
-                    const int c = v % kPerTile;
-                    if (c >= 3 && partial && v / kPerTile == n_tiles - 1) tc::mbar_wait(&sm.v_last[c - 3], 0, &drain);
+                if (loaded) tc::mbar_wait(&sm.q_full, (loaded - 1) & 1, &drain);
+            }
+        } else if (warp == 9) {
+            // ---------------- keys and values: the ring's units in the order of their use
+            const bool leader = tc::elect_one();
+            int u = 0, partials = 0, last[2] = {-kUnits, -kUnits};  // next unit; partial tiles so far, and the units of the latest
+            bool ok = true;
+            while (ok && next_item(p)) {
+                const int n_tiles = tiles(p);
+                if (leader && n_tiles > 0) {
+                    const bool partial = is_partial(p);
+                    const int hk = a.kh ? p.h : 0, hv = a.vh ? p.h : 0;
+                    for (int j = 0; j < n_tiles && ok; ++j) {
+                        if (j == max(0, n_tiles - kAskAhead)) tc::mbar_arrive(&sm.ask);
+                        const int row = p.k0 + j * kN;
+                        for (int c = 0; c < kPerTile; ++c, ++u) {
+                            const int s = u % kUnits;
+                            ok = tc::mbar_wait(&sm.empty[s], ((u / kUnits) + 1) & 1, abort_flag);
+                            uint64_t* bar = &sm.full[s];
+                            if (ok && c >= 3 && partial && j == n_tiles - 1) {
+                                // The V units of a partial last tile pass through warp 10, which then completes `full`; it must be
+                                // through with the latest one (unless that unit's place has been used again since).
+                                const int w = last[c - 3];
+                                if (w > u - kUnits && partials > 0) ok = tc::mbar_wait(&sm.full[w % kUnits], (w / kUnits) & 1, abort_flag);
+                                bar = &sm.v_last[c - 3];
+                                last[c - 3] = u;
+                            }
+                            if (!ok) break;
+                            tc::mbar_expect_tx(bar, kUnitBytes);
+                            if (c < 2) tc::tma_load_3d(sm.ring[s], &kmap, bar, c * 64, hk, row);
+                            else if (c == 2) tc::tma_load_2d(sm.ring[s], &rmap, bar, 0, row);
+                            else {
+                                tc::tma_load_3d(sm.ring[s], &vmap, bar, 0, hv, row + (c - 3) * 64);
+                                tc::tma_load_3d(sm.ring[s] + 8192, &vmap, bar, 64, hv, row + (c - 3) * 64);
+                            }
+                        }
+                    }
+                    if (partial) ++partials;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            // No copy outlives the CTA: all have landed, at once unless a wait gave up.
+            if (leader) {
+                volatile int drain = 0;
+                for (int v = max(0, u - kUnits); v < u; ++v) {
+                    const int c = v == last[0] ? 0 : (v == last[1] ? 1 : -1);
+                    if (c >= 0 && !ok) tc::mbar_wait(&sm.v_last[c], (partials + 1) & 1, &drain);
                     else tc::mbar_wait(&sm.full[v % kUnits], (v / kUnits) & 1, &drain);
                 }
             }
         } else if (warp == 8) {
             // ---------------- MMA issuer
             const uint32_t idesc_s = tc::idesc_f16(kM, kN, 1), idesc_o = tc::idesc_f16_bmn(kM, kDv, 1);
-            if (tc::elect_one() && n_tiles > 0 && tc::mbar_wait(&sm.q_full, 0, abort_flag)) {
-                bool ok = true;
-                auto unit = [&](int j, int c) { return (j * kPerTile + c) % kUnits; };
-                auto landed = [&](int j, int c) {
-                    const int u = j * kPerTile + c;
-                    ok = ok && tc::mbar_wait(&sm.full[u % kUnits], (u / kUnits) & 1, abort_flag);
-                };
-                auto score = [&](int t, int j) {             // S_t = Q_t K_j^T
+            const bool leader = tc::elect_one();
+            int u0 = 0, items = 0, done0 = 0, done1 = 0;           // the item's first unit; items with keys; score tiles before it
+            bool ok = true, any = false;
+            while (ok && next_item(p)) {
+                const int n_tiles = tiles(p);
+                if (leader && n_tiles > 0) {
+                    auto unit = [&](int j, int c) { return (u0 + j * kPerTile + c) % kUnits; };
+                    auto landed = [&](int j, int c) {
+                        const int u = u0 + j * kPerTile + c;
+                        ok = ok && tc::mbar_wait(&sm.full[u % kUnits], (u / kUnits) & 1, abort_flag);
+                    };
+                    auto score = [&](int t, int j) {             // S_t = Q_t K_j^T
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        landed(j, c);
-                        if (!ok) return;
-                        const uint32_t qa = tc::smem_u32(sm.q[t][c]), ka = tc::smem_u32(sm.ring[unit(j, c)]);
+                        for (int c = 0; c < 3; ++c) {
+                            landed(j, c);
+                            if (!ok) return;
+                            const uint32_t qa = tc::smem_u32(sm.q[t][c]), ka = tc::smem_u32(sm.ring[unit(j, c)]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_f16_ss(tmem + t * kN, tc::sdesc_sw128(qa + k * 32), tc::sdesc_sw128(ka + k * 32),
-                                           idesc_s, (c | k) != 0);
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_f16_ss(tmem + t * kN, tc::sdesc_sw128(qa + k * 32), tc::sdesc_sw128(ka + k * 32),
+                                               idesc_s, (c | k) != 0);
+                        }
+                        tc::mma_commit(&sm.s_full[t]);
+                    };
+                    auto weigh = [&](int t, int j, int done) {   // O_t += P_t V_j
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            landed(j, 3 + hf);
+                            ok = ok && tc::mbar_wait(&sm.p_full[t][hf], (done + j) & 1, abort_flag);
+                            if (!ok) return;
+                            tc::tc_fence_after();
+                            const uint32_t va = tc::smem_u32(sm.ring[unit(j, 3 + hf)]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_f16_ts(tmem + 256 + t * kDv, tmem + t * kN + hf * 32 + k * 8,
+                                               tc::sdesc_sw128_lbo(va + k * 2048, 8192, 1024), idesc_o, (j | hf | k) != 0);
+                        }
+                        if (j == p.n[t] - 1) tc::mma_commit(&sm.o_done[t]);
+                    };
+                    auto release = [&](int j, int c0, int c1) {
+                        for (int c = c0; c < c1; ++c) tc::mma_commit(&sm.empty[unit(j, c)]);
+                    };
+                    any = true;
+                    ok = tc::mbar_wait(&sm.q_full, items & 1, abort_flag);
+                    // One step ahead of the products: j = -1 issues the first scores only.
+#pragma unroll 1
+                    for (int j = -1; j < n_tiles && ok; ++j) {
+                        if (j >= 0 && j < p.n[0]) weigh(0, j, done0);
+                        if (ok && j + 1 < p.n[0]) score(0, j + 1);
+                        if (ok && j >= 0 && j < p.n[1]) weigh(1, j, done1);
+                        if (ok && j >= 0) release(j, 3, 5);
+                        if (ok && j + 1 < p.n[1]) score(1, j + 1);
+                        if (ok && j + 1 < n_tiles) release(j + 1, 0, 3);
+                        if (ok && j + 2 == n_tiles) tc::mma_commit(&sm.q_free);    // the last scores are issued
                     }
-                    tc::mma_commit(&sm.s_full[t]);
-                };
-                auto weigh = [&](int t, int j) {             // O_t += P_t V_j
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        landed(j, 3 + hf);
-                        ok = ok && tc::mbar_wait(&sm.p_full[t][hf], j & 1, abort_flag);
-                        if (!ok) return;
-                        tc::tc_fence_after();
-                        const uint32_t va = tc::smem_u32(sm.ring[unit(j, 3 + hf)]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_f16_ts(tmem + 256 + t * kDv, tmem + t * kN + hf * 32 + k * 8,
-                                           tc::sdesc_sw128_lbo(va + k * 2048, 8192, 1024), idesc_o, (j | hf | k) != 0);
-                    }
-                    if (j == p.n[t] - 1) tc::mma_commit(&sm.o_done[t]);
-                };
-                auto release = [&](int j, int c0, int c1) {
-                    for (int c = c0; c < c1; ++c) tc::mma_commit(&sm.empty[unit(j, c)]);
-                };
-                if (p.n[0] > 0) score(0, 0);
-                if (ok && p.n[1] > 0) score(1, 0);
-                if (ok) release(0, 0, 3);
-                for (int j = 0; j < n_tiles && ok; ++j) {
-                    if (j < p.n[0]) weigh(0, j);
-                    if (ok && j + 1 < p.n[0]) score(0, j + 1);
-                    if (ok && j < p.n[1]) weigh(1, j);
-                    if (ok) release(j, 3, 5);
-                    if (ok && j + 1 < p.n[1]) score(1, j + 1);
-                    if (ok && j + 1 < n_tiles) release(j + 1, 0, 3);
+                    ++items;
+                    done0 += p.n[0];
+                    done1 += p.n[1];
+                    u0 += n_tiles * kPerTile;
                 }
-                // Drain before TMEM is freed: a commit completes after every MMA issued.
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            // Drain before TMEM is freed: a commit completes after every MMA issued.
+            if (leader && any) {
                 volatile int drain = 0;
                 if (!ok) *abort_flag = 1;
                 tc::mma_commit(&sm.mma_done);
                 tc::mbar_wait(&sm.mma_done, 0, &drain);
             }
-        } else if (warp == 10 && partial && n_tiles > 0) {
-            // ---------------- rows of the last tile behind the sequence: zero
-            const int j = n_tiles - 1, from = p.nk - j * kN;
-            for (int hf = 0; hf < 2; ++hf) {
-                if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.v_last[hf], 0, abort_flag))) break;
-                const int s = (j * kPerTile + 3 + hf) % kUnits, r0 = max(0, from - hf * 64);
-                for (int i = lane; i < (64 - min(64, r0)) * 16; i += 32)
-                    *reinterpret_cast<uint4*>(sm.ring[s] + ((i >> 3) & 1) * 8192 + (r0 + (i >> 4)) * 128 + (i & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sm.full[s]);
+        } else {
+            // ---------------- rows of a partial last tile behind the sequence: zero
+            int u0 = 0, partials = 0;
+            bool ok = true;
+            while (ok && next_item(p)) {
+                const int n_tiles = tiles(p);
+                if (n_tiles > 0 && is_partial(p)) {
+                    const int j = n_tiles - 1, from = p.nk - j * kN;
+                    for (int hf = 0; hf < 2; ++hf) {
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.v_last[hf], partials & 1, abort_flag));
+                        if (!ok) break;
+                        const int s = (u0 + j * kPerTile + 3 + hf) % kUnits, r0 = max(0, from - hf * 64);
+                        for (int i = lane; i < (64 - min(64, r0)) * 16; i += 32)
+                            *reinterpret_cast<uint4*>(sm.ring[s] + ((i >> 3) & 1) * 8192 + (r0 + (i >> 4)) * 128 + (i & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&sm.full[s]);
+                    }
+                    ++partials;
+                }
+                u0 += n_tiles * kPerTile;
             }
         }
     } else {
@@ -241,114 +368,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + t * kN + lane_off, o_col = tmem + 256 + t * kDv + lane_off;
-        const int n = p.n[t], i = p.i0 + t * kM + row;
-        const bool live = t * kM + row < p.rows;
-        const int lim = a.causal ? min(p.nk, max(0, i + 1 + p.shift)) : p.nk;     // keys this row sees
         const float sc = a.sm_scale_log2;
-        float m = kNegInf, l = 0.f;                  // reference maximum (log2 units) and sum
+        int done = 0, outs = 0;                      // score tiles, and items with keys, of this query tile so far
         bool alive = true;
-        for (int j = 0; j < n; ++j) {
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[t], j & 1, abort_flag))) { alive = false; break; }
-            tc::tc_fence_after();
-            uint32_t w[4][32];
+        Item p;
+        while (alive && next_item(p)) {
+            const int n = p.n[t], i = p.i0 + t * kM + row;
+            const bool live = t * kM + row < p.rows;
+            const int lim = a.causal ? min(p.nk, max(0, i + 1 + p.shift)) : p.nk;     // keys this row sees
+            float m = kNegInf, l = 0.f;              // reference maximum (log2 units) and sum
+            for (int j = 0; j < n; ++j, ++done) {
+                if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[t], done & 1, abort_flag))) { alive = false; break; }
+                tc::tc_fence_after();
+                uint32_t w[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, w[c]);
-            tc::tmem_wait_ld();
-            const int left = lim - j * kN;           // keys of this tile that the row sees
-            if (__any_sync(0xffffffffu, left < kN)) {
+                for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, w[c]);
+                tc::tmem_wait_ld();
+                const int left = lim - j * kN;           // keys of this tile that the row sees
+                if (__any_sync(0xffffffffu, left < kN)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e >= left) w[c][e] = 0xff800000u;
-            }
-            float mx[4];
+                        for (int e = 0; e < 32; ++e)
+                            if (c * 32 + e >= left) w[c][e] = 0xff800000u;
+                }
+                float mx[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = __uint_as_float(w[c][0]);
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(w[c][0]);
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(w[c][e]));
-            }
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-            // The reference rises only when the tile exceeds it by more than 2^8; weights stay below 2^8.
-            float alpha = 1.f;
-            bool rescale = false;
-            if (mt > m + 8.f) {
-                if (m != kNegInf) { alpha = ex2(m - mt); rescale = true; }
-                l *= alpha;
-                m = mt;
-            }
-            if (__any_sync(0xffffffffu, rescale)) {  // O holds P V of the tiles before: their MMAs precede this S
+                    for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(w[c][e]));
+                }
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                // The reference rises only when the tile exceeds it by more than 2^8; weights stay below 2^8.
+                float alpha = 1.f;
+                bool rescale = false;
+                if (mt > m + 8.f) {
+                    if (m != kNegInf) { alpha = ex2(m - mt); rescale = true; }
+                    l *= alpha;
+                    m = mt;
+                }
+                if (__any_sync(0xffffffffu, rescale)) {  // O holds P V of the tiles before: their MMAs precede this S
 #pragma unroll 1
-                for (int c = 0; c < kDv / 32; ++c) {
-                    uint32_t ov[32];
+                    for (int c = 0; c < kDv / 32; ++c) {
+                        uint32_t ov[32];
+                        tc::tmem_ld32(o_col + c * 32, ov);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tc::tmem_st32(o_col + c * 32, ov);
+                    }
+                }
+                const float mref = m == kNegInf ? 0.f : m;
+                const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-mref, -mref);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const uint32_t* s2 = &w[2 * hf + c][e];
+                            float2 x = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])), sc2, m2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            sum[(e >> 1) & 1].x += x.x;
+                            sum[(e >> 1) & 1].y += x.y;
+                            pw[c * 16 + e / 2] = pack_bf16x2(x.x, x.y);
+                        }
+                    tc::tmem_st32(s_col + hf * 32, pw);
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sm.p_full[t][hf]);
+                }
+                l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+            }
+            if (n > 0 && alive) {
+                alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_done[t], outs & 1, abort_flag));
+                ++outs;
+            }
+            tc::tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const size_t orow = (size_t)(p.q0 + t * kM + row) * a.H + p.h;
+#pragma unroll 1
+            for (int c = 0; c < kDv / 32; ++c) {
+                uint32_t ov[32];
+                if (n > 0 && alive) {
                     tc::tmem_ld32(o_col + c * 32, ov);
                     tc::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                    tc::tmem_st32(o_col + c * 32, ov);
-                }
-            }
-            const float mref = m == kNegInf ? 0.f : m;
-            const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-mref, -mref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t pw[32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint32_t* s2 = &w[2 * hf + c][e];
-                        float2 x = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])), sc2, m2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum[(e >> 1) & 1].x += x.x;
-                        sum[(e >> 1) & 1].y += x.y;
-                        pw[c * 16 + e / 2] = pack_bf16x2(x.x, x.y);
-                    }
-                tc::tmem_st32(s_col + hf * 32, pw);
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sm.p_full[t][hf]);
-            }
-            l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-        }
-        if (n > 0 && alive) alive = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_done[t], 0, abort_flag));
-        tc::tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const size_t orow = (size_t)(p.q0 + t * kM + row) * a.H + h;
-#pragma unroll 1
-        for (int c = 0; c < kDv / 32; ++c) {
-            uint32_t ov[32];
-            if (n > 0 && alive) {
-                tc::tmem_ld32(o_col + c * 32, ov);
-                tc::tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] = 0u;
-            }
-            __syncwarp();
-            if (live) {
-                float f[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
-                if (a.o_f32) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + c * 32);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kDv + c * 32);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                            pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                    for (int e = 0; e < 32; ++e) ov[e] = 0u;
                 }
+                __syncwarp();
+                if (live) {
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                    if (a.o_f32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * kDv + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                                pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (live && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
+            tc::tc_fence_before();                   // the next item's first product overwrites O after this warp's p_full
         }
-        if (live && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
     }
     __syncwarp();
     tc::tc_fence_before();
