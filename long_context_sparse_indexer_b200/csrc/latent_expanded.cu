@@ -433,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float2 x = ffma2(make_float2(__uint_as_float(s2[0]), __uint_as_float(s2[1])), sc2, m2);
                             x.x = ex2(x.x);
                             x.y = ex2(x.y);
-                            sum[(e >> 1) & 1].x += x.x;
-                            sum[(e >> 1) & 1].y += x.y;
+                            sum[(e >> 1) & 1] = ffma2(x, make_float2(1.f, 1.f), sum[(e >> 1) & 1]);
                             pw[c * 16 + e / 2] = pack_bf16x2(x.x, x.y);
                         }
                     tc::tmem_st32(s_col + hf * 32, pw);
