@@ -339,6 +339,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 s.k1 = (int)min((long long)s.n, s.k0 + hi - lo);
                 sm.seg[0] = s;
                 tc::mbar_arrive(&sm.seg_full[0]);
+                // Its queries, too: the first two stages are free.
+                const int g = u / k.m_tiles, q0 = g * k.group_rows + (u - g * k.m_tiles) * kM + rank * kRows;
+                tc::mbar_expect_tx(&sm.q_full, 2 * kStageBytes);
+                for (int i = 0; i < 2; ++i) tc::tma_load_3d(sm.ring[i], &qmap, &sm.q_full, 0, q0 + i * 32, 0);
                 if (rank == 0) {
                     WsHeader* w = static_cast<WsHeader*>(a.ws);
                     w->unit[cluster] = u;
@@ -369,10 +373,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         return ok && s.unit >= 0;
     };
     // Queries of a segment into the two stages at ring position r (one warp).  The segment before must have taken
-    // its own: their barrier counts one phase at a time.
+    // its own: their barrier counts one phase at a time.  The first segment's are on their way since the plan.
     auto load_q = [&](const Seg& s, int r, int seg) -> bool {
+        if (seg == 0) return true;
         const int g = s.unit / k.m_tiles, q0 = g * k.group_rows + (s.unit - g * k.m_tiles) * kM + rank * kRows;
-        bool ok = seg == 0 || __all_sync(0xffffffffu, wait(&sm.q_taken, (seg - 1) & 1, abort_flag));
+        bool ok = __all_sync(0xffffffffu, wait(&sm.q_taken, (seg - 1) & 1, abort_flag));
         for (int i = 0; i < 2 && ok; ++i) {
             ok = __all_sync(0xffffffffu, wait(&sm.empty[(r + i) % kStages], (((r + i) / kStages) + 1) & 1, abort_flag));
             if (ok && lane == 0) {
@@ -1009,13 +1014,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 }
 
 // Joins the partial results of the units that a run's start cuts.  Block (c, y): run c + 1's first unit, when that run
-// is the first to start inside it; CTA rows y / 16, 16 dims of each half-row per thread (thread = lane of the partial
-// results).  Weights exp(lse - max), parts in key order.  Launched while the attention still runs: it waits for its end.
-__global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentKernelArgs k) {
+// is the first to start inside it; a CTA's rows and 4 V dims of each half-row.  Thread = lane of the partial results, in
+// one of P groups; a group takes every P-th part in key order with weights exp(lse - its own maximum), and the groups'
+// results are joined in order the same way.  Launched while the attention still runs: it waits for its end.
+template <int V, int P>
+__global__ void __launch_bounds__(128 * P) latent_merge_kernel(const __grid_constant__ LatentKernelArgs k) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const LatentArgs& a = k.a;
     const WsHeader* ws = static_cast<const WsHeader*>(a.ws);
     __shared__ WsHeader sh;                      // read at once: the runs of a unit are counted one after another
+    __shared__ float4 acc_s[P > 1 ? P - 1 : 1][V][P > 1 ? 128 : 1];
+    __shared__ float2 stat_s[P > 1 ? P - 1 : 1][P > 1 ? 128 : 1];
     WsHeader* w = &sh;
     for (int i = threadIdx.x; i < kMaxClusters; i += blockDim.x) { w->unit[i] = ws->unit[i]; w->k0[i] = ws->k0[i]; }
     const int c = blockIdx.x + 1, n_runs = ws->clusters;
@@ -1025,46 +1034,75 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant
     if (w->unit[c - 1] == u && w->k0[c - 1] > 0) return;           // an earlier run is the first
     int last = c;
     while (last + 1 < n_runs && w->unit[last + 1] == u) ++last;    // every later run of the unit starts inside it
-    const int rank = blockIdx.y >> 4, c4 = (blockIdx.y & 15) * 4, L = threadIdx.x, row = L & 63;
+    constexpr int kSlices = 64 / V;
+    const int rank = blockIdx.y / kSlices, c4 = (blockIdx.y % kSlices) * V;
+    const int L = threadIdx.x & 127, part = threadIdx.x >> 7, row = L & 63;
     const int g = u / k.m_tiles, grow = (u - g * k.m_tiles) * kM + rank * kRows + row;
-    if (grow >= k.group_rows) return;
+    const bool live = grow < k.group_rows;
     auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
     const int n = last - c + 2;
-    float m = kNegInf;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) m = fmaxf(m, part_lse(a.ws, slot(i))[rank * kRows + row]);
-    float acc[16], sum = 0.f;
+    float m = kNegInf, sum = 0.f;
+    float4 acc[V];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    for (int e = 0; e < V; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int e, float x, float4 v) {
+        acc[e].x = fmaf(x, v.x, acc[e].x);
+        acc[e].y = fmaf(x, v.y, acc[e].y);
+        acc[e].z = fmaf(x, v.z, acc[e].z);
+        acc[e].w = fmaf(x, v.w, acc[e].w);
+    };
+    if (live) {
 #pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float lse = part_lse(a.ws, slot(i))[rank * kRows + row];
-        const float wt = lse == kNegInf ? 0.f : expf(lse - m);     // a part without keys holds zeros
-        const float4* p = part_o(a.ws, slot(i), rank) + (size_t)c4 * 128 + L;
-        sum += wt;
+        for (int i = part; i < n; i += P) m = fmaxf(m, part_lse(a.ws, slot(i))[rank * kRows + row]);
+#pragma unroll 8
+        for (int i = part; i < n; i += P) {
+            const float lse = part_lse(a.ws, slot(i))[rank * kRows + row];
+            const float x = lse == kNegInf ? 0.f : expf(lse - m);  // a part without keys holds zeros
+            const float4* p = part_o(a.ws, slot(i), rank) + (size_t)c4 * 128 + L;
+            sum += x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 v = p[e * 128];
-            acc[4 * e] = fmaf(wt, v.x, acc[4 * e]);
-            acc[4 * e + 1] = fmaf(wt, v.y, acc[4 * e + 1]);
-            acc[4 * e + 2] = fmaf(wt, v.z, acc[4 * e + 2]);
-            acc[4 * e + 3] = fmaf(wt, v.w, acc[4 * e + 3]);
+            for (int e = 0; e < V; ++e) add(e, x, p[e * 128]);
         }
     }
+    if constexpr (P > 1) {
+        if (part > 0) {
+            stat_s[part - 1][L] = make_float2(m, sum);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc_s[part - 1][e][L] = acc[e];
+        }
+        __syncthreads();
+        if (part > 0) return;
+        float mm = m;
+#pragma unroll
+        for (int j = 0; j < P - 1; ++j) mm = fmaxf(mm, stat_s[j][L].x);
+        const float x0 = m == kNegInf ? 0.f : expf(m - mm);
+        sum *= x0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = make_float4(acc[e].x * x0, acc[e].y * x0, acc[e].z * x0, acc[e].w * x0);
+#pragma unroll
+        for (int j = 0; j < P - 1; ++j) {
+            const float2 t = stat_s[j][L];
+            const float x = t.x == kNegInf ? 0.f : expf(t.x - mm);
+            sum = fmaf(x, t.y, sum);
+#pragma unroll
+            for (int e = 0; e < V; ++e) add(e, x, acc_s[j][e][L]);
+        }
+        m = mm;
+    }
+    if (!live) return;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] *= inv;
+    for (int e = 0; e < V; ++e) acc[e] = make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
     const size_t orow = (size_t)g * k.group_rows + grow, at = orow * kDv + (L >> 6) * 256 + c4 * 4;
     if (a.o_f32) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            reinterpret_cast<float4*>(static_cast<float*>(a.o) + at)[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+        for (int e = 0; e < V; ++e) reinterpret_cast<float4*>(static_cast<float*>(a.o) + at)[e] = acc[e];
     } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at)[e] =
-                make_uint4(pack_bf16x2(acc[8 * e], acc[8 * e + 1]), pack_bf16x2(acc[8 * e + 2], acc[8 * e + 3]),
-                           pack_bf16x2(acc[8 * e + 4], acc[8 * e + 5]), pack_bf16x2(acc[8 * e + 6], acc[8 * e + 7]));
+        for (int e = 0; e < V; e += 2)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at)[e / 2] =
+                make_uint4(pack_bf16x2(acc[e].x, acc[e].y), pack_bf16x2(acc[e].z, acc[e].w),
+                           pack_bf16x2(acc[e + 1].x, acc[e + 1].y), pack_bf16x2(acc[e + 1].z, acc[e + 1].w));
     }
     if (L < kRows && c4 == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
 }
@@ -1130,15 +1168,19 @@ cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtenso
     if (e != cudaSuccess || k.clusters == 1) return e;
     // The join is launched while the attention runs, and waits for its end on the device.
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(k.clusters - 1, 32);
-    cfg.blockDim = dim3(128);
+    // Units of eight parts and more: four groups of a block share them.  Units of few: small blocks that wait resident
+    // beside the attention (12 units of 6 parts 45.9 us so, 50.4 in groups; one token at 48752 rows, 74 parts, 46.4 us in
+    // groups and 73 in one).
+    const bool wide = k.units * 8 <= k.clusters;
+    cfg.gridDim = dim3(k.clusters - 1, wide ? 64 : 32);
+    cfg.blockDim = dim3(wide ? 512 : 128);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_merge_kernel, k);
+    return wide ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<2, 4>, k) : cudaLaunchKernelEx(&cfg, latent_merge_kernel<4, 1>, k);
 }
 
 }  // namespace
