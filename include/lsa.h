@@ -314,7 +314,8 @@ typedef struct {
  *   2. with `rope`, elements rope_off .. rope_off + rot_dim - 1 are rotated by q_pos[t];
  *   3. the row is stored as BF16, or as e4m3 codes with scale = max|row| / 448 (1 for a row of zeros),
  *      code = row * (448 / max|row|) rounded to nearest even.
- * All in 32 bits, rounded once.  A latent row is [norm_dim = 512 normalised | 64 rotated]; an indexer key is
+ * All in 32 bits, rounded once (|x| below 2^59 in a normalised part, so that its sum of squares is finite).  A
+ * latent row is [norm_dim = 512 normalised | 64 rotated]; an indexer key is
  * layer-normalised whole and rotated in part.  A token with q_pos[t] < 0 is padding: nothing is stored.
  * A row with a NaN or an infinity is reported (LSA_ERR_DEVICE_DATA) and stored as it is in a BF16 cache, as
  * NaN codes with scale 1 in an FP8 cache; a position outside the sequence, or a bad page, is reported and
@@ -336,7 +337,7 @@ lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x,
  * (q_group) belong to one sequence, that of the group's first token, and read its rows together.  A token
  * with q_pos[t] < 0 is padding: o = 0, lse = -inf.  A position or a sequence outside the batch is reported
  * and its token treated as padding.  Cached values at rows 0 .. the group's largest q_pos must be finite;
- * what lies behind them may be anything.
+ * what lies behind them may be anything.  With an FP8 cache |q| < 2^67 and scale * sm_scale < 2^58.
  *   q [T][H][576] BF16; o [T][H][512] of out_dtype (LSA_BF16, or LSA_FP32 for results that are merged later
  *   with lsa_merge_partials); lse [T][H] float or NULL.  1 <= H <= 1024, q_group * H < 2^31 / 1024.
  *   The work is cut evenly over the GPU by rows read, so ragged lengths need no split count; partial

@@ -273,7 +273,15 @@ __global__ void __launch_bounds__(256, SLOTS == 1 ? 4 : 3) append_kernel(const _
         if (ok && bad) report(p.status, LSA_ERR_DEVICE_DATA);
         uint8_t* dst = p.data + off;
         if constexpr (FP8) {
-            const float inv = amax > 0.f ? 448.f / amax : 1.f;
+            // 448 / amax would overflow for the tiniest rows: those are taken 2^64 times.
+            const float up = amax < 0x1p-60f ? 0x1p64f : 1.f;
+            if (up != 1.f) {
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[s][e] = mul2(v[s][e], make_float2(up, up));
+            }
+            const float inv = amax > 0.f ? 448.f / (amax * up) : 1.f;
             const int64_t sc = __shfl_sync(0xffffffffu, my_sc, i * kSide + side);
             if (ok && lane == 0) p.scale[sc] = bad || !(amax > 0.f) ? 1.f : amax / 448.f;
 #pragma unroll

@@ -101,6 +101,15 @@ def test_rope_strided_views(cuda, dtype, inter):
     _rope_close(y, one, pos, r, 0)
 
 
+def test_rope_far_rows(cuda):
+    """Tokens 2^31 + 64 elements apart."""
+    x, pos, r = _normal(_gen(8), 3, 2, 128), _ints(5, 900, 77), lsa.Rope(64)
+    far = torch.empty(2 ** 32 + 4096, dtype=torch.bfloat16, device=DEV).as_strided((3, 2, 128), (2 ** 31 + 64, 128, 1))
+    far.copy_(x)
+    lsa.rope(r, pos, far, offset=64)
+    assert torch.equal(far, lsa.rope(r, pos, x, torch.empty_like(x), offset=64))
+
+
 def test_rope_far_and_negative_positions(cuda):
     """Angles at the ends of int32 keep their fraction of a turn (64 bits: 2^31 rad within 2^-21)."""
     r = lsa.Rope(64, interleaved=True)
@@ -257,6 +266,46 @@ def test_append_padding_bad_tokens_and_bad_values(cuda):
     data, _, st = run([0, 1], [0, 1], bad, fp8=False)
     assert st == lsa.ERR_DEVICE_DATA and data[0, 0].isnan().sum() == 1
     assert torch.equal(data[0, 0, 100:], bad[0, 100:])
+
+
+def test_append_tiny_rows(cuda):
+    """Rows down to the smallest BF16 subnormal, where 448 / max|row| overflows: codes as for any other row, the scale
+    rounded to a 32-bit subnormal (half a step of 2^-149, times codes of at most 448)."""
+    x = _normal(_gen(9), 8, 128)
+    x = (x.double() * torch.tensor([2.0 ** -e for e in (30, 59, 61, 64, 100, 124, 127, 130)], device=DEV)[:, None]).to(torch.bfloat16)
+    x[:, 3] = 0
+    st, data = _status(), torch.zeros(1, 8, 128, dtype=torch.uint8, device=DEV)
+    scale = torch.zeros(1, 8, device=DEV)
+    lsa.cache_append(lsa.Batch(_ints(8), _ints(*[0] * 8), _ints(*range(8)), 8), x, lsa.Cache(data, scale), dev_status=st)
+    assert lsa.read_device_status(st) == lsa.OK
+    v, y = data.view(E4M3).double()[0] * scale.double()[0, :, None], x.double()
+    step = 2.0 ** -4 * y.abs() * (1 + 2.0 ** -20) + 2.0 ** -10 * scale.double()[0, :, None] + 448 * 2.0 ** -150 * (1 + 2.0 ** -4)
+    assert v.isfinite().all() and ((v - y).abs() <= step).all()
+
+
+def test_append_far_rows(cuda):
+    """Rows more than 2^32 bytes into a pool, and sequences as far apart."""
+    x, r = _normal(_gen(3), 6, 576), lsa.Rope(64, interleaved=True)
+    q_seq, q_pos = _ints(0, 0, 0, 1, 1, 1), _ints(5, 6, 70, 0, 64, 99)
+    for fp8 in (False, True):
+        dt, n = (torch.uint8, 120000) if fp8 else (torch.bfloat16, 60000)
+        run = lambda cache, pages: lsa.cache_append(lsa.Batch(_ints(100, 100), q_seq, q_pos, 100), x, cache, pages=pages,  # noqa: E731
+                                                    norm="rms", norm_dim=512, rope=r, rope_offset=512)
+        small = torch.zeros(2, 100, 576, dtype=dt, device=DEV)
+        ss = torch.zeros(2, 100, device=DEV) if fp8 else None
+        run(lsa.Cache(small, ss), None)
+        want = small[q_seq.long(), q_pos.long()]
+        pool = torch.empty(n, 64, 576, dtype=dt, device=DEV)
+        ps = torch.zeros(n, 64, device=DEV) if fp8 else None
+        table = _ints(n - 1, n - 3, n - 2, n - 9).view(2, 2)
+        run(lsa.Cache(pool, ps), lsa.PageTable(table))
+        at = (table[q_seq.long(), (q_pos // 64).long()].long(), (q_pos % 64).long())
+        assert torch.equal(pool[at], want) and (ps is None or torch.equal(ps[at], ss[q_seq.long(), q_pos.long()]))
+        far = pool.view(-1).as_strided((2, 100, 576), (pool.numel() - 100 * 576, 576, 1))
+        fs = torch.zeros(2, 100, device=DEV) if fp8 else None
+        run(lsa.Cache(far, fs), None)
+        assert torch.equal(far[q_seq.long(), q_pos.long()], want)
+        del pool, far
 
 
 # ------------------------------------------------------------------ latent attention, absorbed form
@@ -503,6 +552,87 @@ def test_latent_twice_the_same_and_on_other_streams(cuda):
     s.check("replay")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_latent_far_rows(cuda, fp8):
+    """Pages more than 2^32 bytes into their pool, and sequences as far apart."""
+    s = Latent(51, 16, [300, 131], _tail([300, 131], 2), page=64, fp8=fp8)
+    n = 120000 if fp8 else 60000
+    pool = torch.empty(n, 64, 576, dtype=s.cache.data.dtype, device=DEV)
+    lead = s.cache.data.shape[0]
+    pool[n - lead:] = s.cache.data
+    scale = None
+    if fp8:
+        scale = torch.empty(n, 64, device=DEV)
+        scale[n - lead:] = s.cache.scale
+    s.cache = lsa.Cache(pool, scale)
+    s.pages.table[s.pages.table >= 0] += n - lead
+    s.run()
+    s.check("pages")
+    z = Latent(52, 16, [300, 131], _tail([300, 131], 2), page=0, fp8=fp8)
+    far = pool.view(-1).as_strided((2, 300, 576), (pool.numel() - 300 * 576, 576, 1))
+    far.copy_(z.cache.data)
+    z.cache = lsa.Cache(far, z.cache.scale)
+    z.run()
+    z.check("sequences")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_latent_sequences_side_by_side_and_shared(cuda, fp8):
+    """Sequences as columns of one [rows, sequences, 576] tensor, all sequences on the same rows (stride 0), and two
+    sequences whose tables name the same pages."""
+    s = Latent(61, 20, [200, 333], _tail([200, 333], 2), page=0, fp8=fp8)
+    s.cache = lsa.Cache(s.cache.data.transpose(0, 1).contiguous().transpose(0, 1), s.cache.scale)
+    s.run()
+    s.check("columns")
+    s = Latent(62, 20, [300, 300], [[299, 298], [70, 299]], page=0, fp8=fp8)
+    s.cache = lsa.Cache(s.cache.data[1:].expand(2, -1, -1), s.cache.scale[1:].expand(2, -1) if fp8 else None)
+    s.rows = s.rows[[1, 1]]
+    s.run()
+    s.check("shared rows")
+    s = Latent(63, 20, [300, 300], [[299, 298], [70, 299]], page=64, fp8=fp8)
+    s.pages.table[0, :4] = s.pages.table[1, :4]
+    s.rows[0, :256] = s.rows[1, :256]
+    s.run()
+    s.check("shared pages")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,lens", [(20, [30000]), (128, [30000]), (200, [9000]), (128, [20000] + [50] * 40)])
+def test_latent_units_of_many_parts(cuda, fp8, H, lens):
+    """One context cut over the whole GPU and joined, alone and among short ones, in both output types."""
+    for f32 in (False, True):
+        s = Latent(70 + H, H, lens, _tail(lens, 1), fp8=fp8, f32=f32, scale=0.5)
+        s.run()
+        s.check()
+
+
+def test_first_calls_of_a_process_are_captured(cuda):
+    """A process whose first calls are captured replays them."""
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = ["tests", "."]
+import torch
+import test_gpu_latent_ops as t
+s, z, e = t.Latent(1, 128, [700], [[699]]), t.Latent(2, 16, [700], [[699]], fp8=True), t.Expanded(3, 4, [300], [400])
+x, y = t._normal(t._gen(4), 5, 3, 64), torch.zeros(5, 3, 64, dtype=torch.bfloat16, device="cuda")
+pos, r, starts = t._ints(0, 1, 2, 3, 4), t.lsa.Rope(64), (t._ints(0, 300), t._ints(0, 400))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    s.run(), z.run(), e.run(starts=starts)
+    t.lsa.rope(r, pos, x, y)
+    t.lsa.cache_append(z.batch, z.q[:1, 0], z.cache, pages=z.pages)
+graph.replay()
+torch.cuda.synchronize()
+s.check(), e.check()
+assert t.lsa.read_device_status(z.st) == t.lsa.OK and z.o.isfinite().all() and torch.equal(x[0], y[0])
+"""
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
+
+
 def test_latent_matches_sparse_attention_over_every_row(cuda):
     """The sparse path given every visible row computes the same attention (contiguous BF16 cache)."""
     lens = [700, 64]
@@ -599,6 +729,20 @@ def test_expanded_strides_gaps_and_32_bit_results(cuda):
     s.run()
     s.check()
     assert torch.equal(o, s.o)
+
+
+def test_expanded_far_rows(cuda):
+    """Tokens 2^28 elements apart: the last ones lie more than 2^32 elements into the tensors."""
+    s = Expanded(14, 2, [20], [20])
+    buf = torch.empty(19 * 2 ** 28 + 8192, dtype=torch.bfloat16, device=DEV)
+
+    def spread(t, off):
+        f = buf[off:].as_strided(t.shape, (2 ** 28, *t.stride()[1:]))
+        return f.copy_(t)
+    s.q, s.kn, s.v, s.kr = spread(s.q, 0), spread(s.kn, 1024), spread(s.v, 2048), spread(s.kr, 4096)
+    s.run()
+    s.check()
+    del buf
 
 
 def test_expanded_extreme_scores(cuda):
