@@ -619,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
                 const bool write = grow < k.group_rows;
                 const size_t orow = (size_t)g * k.group_rows + grow;
-                float4* part = part_o(a.ws, slot, rank) + L;
+                float4* part = part_o(a.ws, slot, rank) + L;        // rows past the group's are not written
                 if (hf == 0 && wg == 0 && write) {
                     if (!whole) part_lse(a.ws, slot)[rank * kRows + row] = lse;
                     else if (a.lse) a.lse[orow] = lse;
@@ -634,8 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
                     if (!whole) {                // lanes side by side
+                        if (write)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) part[(c / 4 + e) * 128] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            for (int e = 0; e < 8; ++e) part[(c / 4 + e) * 128] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                     } else if (a.o_f32) {
                         float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + hf * 256 + c);
                         if (write)
