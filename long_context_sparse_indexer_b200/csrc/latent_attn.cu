@@ -634,14 +634,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
                     if (!whole) {                // lanes side by side
-                        if (write)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) part[(c / 4 + e) * 128] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e)
+                            if (write) part[(c / 4 + e) * 128] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                     } else if (a.o_f32) {
                         float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + hf * 256 + c);
-                        if (write)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e)
+                            if (write) d[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                     } else {                     // 64 bytes of 32 rows through shared memory: 8 rows a store
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
