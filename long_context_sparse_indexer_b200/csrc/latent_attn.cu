@@ -171,11 +171,6 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
         :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-__device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w, int v) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-        :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v) : "memory");
-}
 // Boxes completing on a barrier of this CTA.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int w) {
     asm volatile(
@@ -206,7 +201,6 @@ struct LatentKernelArgs {
     LatentArgs a;
     int units, m_tiles, group_rows;              // units, units of a group, rows of a group
     int clusters;
-    int whole;                                   // a tile's 32 keys of a CTA are one TMA box (pages of whole 32 rows)
 };
 
 // Page (or sequence, without pages) of a sequence's row and its place in it; -1, reported, for a page outside the pool.
@@ -862,8 +856,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + (rank ^ 1) * 4 * kAtom, &xmap, &sm.x_full[st], 0, rw, rank * 4, pg);
                 } else if (FP8) {
                     if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + kCodeAt, &kmap, &sm.code_full[st], 0, rw, 0, pg);
-                } else if (k.whole) {            // 32 rows in one box
-                    if (lane == 0) tma_load_5d_pair(sm.ring[st], &kmap, bar0, 0, 0, 0, rw / 8, pg);
                 } else if (lane < 4) {           // 8 rows a box
                     tma_load_4d_pair(sm.ring[st] + lane * kGroup, &kmap, bar0, 0, rw, 0, pg);
                 }
@@ -1120,18 +1112,6 @@ bool make_kv_map(const LatentArgs& a, CUtensorMap* m, int chunks) {
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// BF16: (64 dims, 8 rows, 9 chunks, groups of 8 rows, pages), box 64 x 8 x 9 x 4 x 1: a CTA's keys of a tile, in a stage's
-// order.
-bool make_tile_map(const LatentArgs& a, CUtensorMap* m) {
-    const bool one = a.n_pages == 1 || a.seq_b == 0;
-    const cuuint64_t d[5] = {64, 8, kAtoms, (cuuint64_t)(a.page_size / 8), (cuuint64_t)(one ? 1 : a.n_pages)};
-    const cuuint64_t s[4] = {(cuuint64_t)a.tok_b, 128, (cuuint64_t)a.tok_b * 8, (cuuint64_t)(one ? a.tok_b : a.seq_b)};
-    const cuuint32_t box[5] = {64, 8, kAtoms, 4, 1}, e[5] = {1, 1, 1, 1, 1};
-    return tc::encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(a.kv), d, s, box, e,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Clusters that run at once on the current device (asked once per device).
 template <bool FP8>
 int cluster_count(size_t smem) {
@@ -1206,10 +1186,7 @@ cudaError_t launch_latent_attn(const LatentArgs& a, cudaStream_t st) {
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    // One box per CTA and tile where pages hold 32 rows whole; a sequence without pages may end inside 8 rows, which
-    // only the map by single rows bounds.
-    k.whole = !a.kv_scale && a.page_size % 32 == 0;
-    if (!(k.whole ? make_tile_map(a, &km) : make_kv_map(a, &km, kAtoms))) return cudaErrorInvalidValue;
+    if (!make_kv_map(a, &km, kAtoms)) return cudaErrorInvalidValue;
     if (!make_kv_map(a, &xm, 4)) return cudaErrorInvalidValue;
     if (a.kv_scale) return launch_t<true>(qm, km, xm, k, st);
     return launch_t<false>(qm, km, xm, k, st);
