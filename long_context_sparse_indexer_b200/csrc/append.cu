@@ -2,7 +2,8 @@
 //
 // h = norm(x[0:n]) (RMS or layer norm), then the rotation of the rotary part, then BF16 or e4m3 codes with
 // scale = max|row| / 448.  Every element is read once and written once with a few operations in between:
-// bound by memory for many rows (and close behind by instructions) and by the latency of one row for few.  LANES lanes
+// bound by memory for many rows (and close behind by instructions) and by the latency of one row for few (32,764 latent
+// rows to BF16 pages 28 us, 2.7 TB/s; as many 128-element keys to FP8 17.7 us; a decode step's 32 rows 4.4 us).  LANES lanes
 // (32, 16 or 8, the fewest that hold a row in up to four 16-byte chunks each) take a row and keep it in registers, so
 // that its loads travel together and the reductions are shuffles.  A warp takes several rows one after another: the
 // loads that find their places depend on one another (position and sequence, then length and page), so lanes find
