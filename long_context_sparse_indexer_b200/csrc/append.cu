@@ -3,7 +3,7 @@
 // h = norm(x[0:n]) (RMS or layer norm), then the rotation of the rotary part, then BF16 or e4m3 codes with
 // scale = max|row| / 448.  Every element is read once and written once with a few operations in between:
 // bound by memory for many rows (and close behind by instructions) and by the latency of one row for few (32,764 latent
-// rows to BF16 pages 28 us, 2.7 TB/s; as many 128-element keys to FP8 17.7 us; a decode step's 32 rows 4.4 us).  LANES lanes
+// rows to BF16 pages 23 us, 3.3 TB/s; as many 128-element keys to FP8 17 us; a decode step's 32 rows 4.4 us).  LANES lanes
 // (32, 16 or 8, the fewest that hold a row in up to four 16-byte chunks each) take a row and keep it in registers, so
 // that its loads travel together and the reductions are shuffles.  A warp takes several rows one after another: the
 // loads that find their places depend on one another (position and sequence, then length and page), so lanes find
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(256, SLOTS == 1 ? 4 : 3) append_kernel(const _
                 if (s * LANES + lane < nc)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sq = ffma2(v[s][e], v[s][e], sq);
-            const float rs = 1.f / sqrtf(lanes_sum<LANES>(sq.x + sq.y) * inv_n + p.eps);
+            const float rs = rsqrtf(lanes_sum<LANES>(sq.x + sq.y) * inv_n + p.eps);
             const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
             for (int s = 0; s < SLOTS; ++s)
@@ -253,6 +253,12 @@ __global__ void __launch_bounds__(256, SLOTS == 1 ? 4 : 3) append_kernel(const _
                 }
             }
         }
+        // The row as it stands here: left to itself the compiler carries every path of the rotation through to its own store, in
+        // more registers than there are (rows to BF16 28 us so, 23 us pinned).
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) asm volatile("" : "+f"(v[s][e].x), "+f"(v[s][e].y));
         // 0 x element: zero, or NaN for an infinity or a NaN.
         float2 none = make_float2(0.f, 0.f);
 #pragma unroll
