@@ -310,7 +310,7 @@ typedef struct {
  * elements; 16-byte aligned rows):
  *   1. the first norm_dim elements are normalised: LSA_NORM_RMS  h = x * rsqrt(mean(x^2) + eps) * gamma,
  *      LSA_NORM_LAYER  h = (x - mean) * rsqrt(var + eps) * gamma + beta (gamma, beta: device FP32
- *      [norm_dim], NULL = ones / zeros); LSA_NORM_NONE leaves them;
+ *      [norm_dim], NULL = ones / zeros); LSA_NORM_NONE leaves them (gamma and beta are not read);
  *   2. with `rope`, elements rope_off .. rope_off + rot_dim - 1 are rotated by q_pos[t];
  *   3. the row is stored as BF16, or as e4m3 codes with scale = max|row| / 448 (1 for a row of zeros),
  *      code = row * (448 / max|row|) rounded to nearest even.
@@ -356,7 +356,7 @@ size_t lsa_latent_attn_workspace_size(int T, int q_group, int H);
  * (device int32 [B + 1], ascending, within 0 .. T and 0 .. S).  causal != 0: its last query sees its last
  * key, query i (of nq) sees keys 0 .. i + nk - nq; a query that sees no key gets o = 0, lse = -inf.
  * Query rows of no sequence are left as they were.  max_q: at least the longest nq (a sequence's queries
- * beyond it are reported and not computed).  Strides in elements, rows 16-byte aligned:
+ * beyond it are reported and not computed; 0: the call does nothing).  Strides in elements, rows 16-byte aligned:
  *   q [T][H][192], k_nope [S][H][128], v [S][H][128], k_rope [S][64], all BF16 -- k_nope and v may be the
  *   halves of one [S][H][256] projection; o [T][H][128] contiguous, of out_dtype (LSA_BF16 or LSA_FP32);
  *   lse [T][H] float or NULL.  Keys and values of a sequence must be finite. */

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -399,13 +400,24 @@ def _int_vec(t: torch.Tensor, n: int, name: str) -> None:
         raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements")
 
 
-def _batch_c(b: Batch, T: int) -> CBatch:
+# lsa_batch, lsa_cache and lsa_pages as packed bytes, which take a quarter of the time of a ctypes structure; the calls below
+# that take them have function objects of their own.
+_pack_batch = struct.Struct("=iiiiQQQ").pack
+_pack_cache = struct.Struct("=QQiiqqq").pack
+_pack_pages = struct.Struct("=Qqiiii").pack
+_cache_append_c, _latent_attn_c = _lib["lsa_cache_append"], _lib["lsa_latent_attn"]
+for _f, _of in ((_cache_append_c, _lib.lsa_cache_append), (_latent_attn_c, _lib.lsa_latent_attn)):
+    _f.argtypes = [c_vp if t in (_P(CBatch), _P(CCache), _P(CPages)) else t for t in _of.argtypes]
+    _f.restype = _of.restype
+
+
+def _batch_c(b: Batch, T: int) -> bytes:
     """The C batch of checked vectors."""
     _int_vec(b.q_seq, T, "q_seq")
     _int_vec(b.q_pos, T, "q_pos")
     B = b.seq_len.numel()
     _int_vec(b.seq_len, B, "seq_len")
-    return CBatch(B, T, b.q_group, b.L_alloc, b.seq_len.data_ptr(), b.q_seq.data_ptr(), b.q_pos.data_ptr())
+    return _pack_batch(B, T, b.q_group, b.L_alloc, b.seq_len.data_ptr(), b.q_seq.data_ptr(), b.q_pos.data_ptr())
 
 
 class Rope:
@@ -443,18 +455,19 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 def _cache_c(cache: Cache, pages: Optional[PageTable], B: int, rows: int):
     """The C cache and page table (None: a cache of the batch's B sequences of at least `rows` rows), checked."""
     d, sc = cache.data, cache.scale
-    if d.dim() != 3:
+    shape = d.shape
+    if len(shape) != 3:
         raise ValueError("cache: [sequences or pages, rows, dim]")
-    n, r, dim = d.shape
+    n, r, dim = shape
     s0, s1, s2 = d.stride()
     if s2 != 1:
         raise ValueError("cache: rows of contiguous elements")
     if d.dtype is torch.bfloat16:
-        cc = CCache(d.data_ptr(), None, BF16, dim, s0, s1, 0)
+        cc = _pack_cache(d.data_ptr(), 0, BF16, dim, s0, s1, 0)
     elif d.dtype in _E4M3:
-        if sc is None or sc.dtype is not torch.float32 or sc.dim() != 2 or sc.size(0) != n or sc.size(1) != r or sc.stride(1) != 1:
+        if sc is None or sc.dtype is not torch.float32 or sc.shape != (n, r) or sc.stride(1) != 1:
             raise ValueError("cache scale: float32 [sequences or pages, rows] with contiguous rows")
-        cc = CCache(d.data_ptr(), sc.data_ptr(), FP8_E4M3, dim, s0, s1, sc.stride(0))
+        cc = _pack_cache(d.data_ptr(), sc.data_ptr(), FP8_E4M3, dim, s0, s1, sc.stride(0))
     else:
         raise ValueError(f"unsupported cache dtype {d.dtype}")
     if pages is None:
@@ -462,12 +475,13 @@ def _cache_c(cache: Cache, pages: Optional[PageTable], B: int, rows: int):
             raise ValueError("cache: fewer sequences or rows than the batch")
         return cc, None
     t = pages.table
-    if t.dim() != 2 or t.dtype is not torch.int32 or t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or t.dtype is not torch.int32 or t.stride(1) != 1:
         raise ValueError("page table: int32 [sequences, pages per sequence] with contiguous rows")
-    tb, tn = t.shape
+    tb, tn = shape
     if tb < B:
         raise ValueError("page table: fewer sequences than the batch")
-    return cc, CPages(t.data_ptr(), t.stride(0) if tb > 1 else tn, tn, r, n, 0)
+    return cc, _pack_pages(t.data_ptr(), t.stride(0) if tb > 1 else tn, tn, r, n, 0)
 
 
 def rope(rope: Rope, pos: torch.Tensor, x: torch.Tensor, y: Optional[torch.Tensor] = None, offset: int = 0,
@@ -508,7 +522,7 @@ def cache_append(batch: Batch, x: torch.Tensor, cache: Cache, pages: Optional[Pa
     if norm not in _NORMS:
         raise ValueError(f"unknown norm {norm!r}")
     T, dim = batch.q_seq.numel(), cache.data.size(-1)
-    if x.dim() != 2 or x.size(0) != T or x.size(1) != dim or x.dtype is not torch.bfloat16 or x.stride(1) != 1:
+    if x.shape != (T, dim) or x.dtype is not torch.bfloat16 or x.stride(1) != 1:
         raise ValueError("cache_append: x is [T, dim] bf16 with contiguous rows")
     norm_dim = norm_dim or dim
     if gamma is not None:
@@ -516,10 +530,10 @@ def cache_append(batch: Batch, x: torch.Tensor, cache: Cache, pages: Optional[Pa
     if beta is not None:
         _float_vec(beta, norm_dim, "beta")
     cb = _batch_c(batch, T)
-    cc, cp = _cache_c(cache, pages, cb.B, batch.L_alloc)
+    cc, cp = _cache_c(cache, pages, batch.seq_len.numel(), batch.L_alloc)
     dev = _launch_device(x, cache.data, cache.scale, gamma, beta, dev_status, batch.q_pos, batch.q_seq, batch.seq_len,
                          None if pages is None else pages.table)
-    _check(_lib.lsa_cache_append(cb, x.data_ptr(), x.stride(0) if T > 1 else dim, _NORMS[norm], norm_dim, _ptr(gamma),
+    _check(_cache_append_c(cb, x.data_ptr(), x.stride(0) if T > 1 else dim, _NORMS[norm], norm_dim, _ptr(gamma),
                                  _ptr(beta), eps, None if rope is None else rope.c, rope_offset, cc, cp,
                                  _ptr(dev_status), _stream_on(dev, stream)), "lsa_cache_append")
 
@@ -548,10 +562,10 @@ def latent_attn(batch: Batch, q: torch.Tensor, cache: Cache, sm_scale: float, o:
     if lse is not None:
         _float_vec(lse, T * H, "lse")
     cb = _batch_c(batch, T)
-    cc, cp = _cache_c(cache, pages, cb.B, batch.L_alloc)
+    cc, cp = _cache_c(cache, pages, batch.seq_len.numel(), batch.L_alloc)
     dev = _launch_device(q, o, lse, ws, dev_status, cache.data, cache.scale, batch.q_pos, batch.q_seq, batch.seq_len,
                          None if pages is None else pages.table)
-    _check(_lib.lsa_latent_attn(cb, q.data_ptr(), H, cc, cp, sm_scale, o.data_ptr(), dt, _ptr(lse), _ptr(ws),
+    _check(_latent_attn_c(cb, q.data_ptr(), H, cc, cp, sm_scale, o.data_ptr(), dt, _ptr(lse), _ptr(ws),
                                 0 if ws is None else ws.numel() * ws.element_size(), _ptr(dev_status),
                                 _stream_on(dev, stream)), "lsa_latent_attn")
 
