@@ -315,14 +315,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     }
     if (lane == 31) sm.scan[warp] = before;
     __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sm.scan[w];
-        total += sm.scan[w];
+    long long sums = lane < kThreads / 32 ? sm.scan[lane] : 0;     // of the warps up to this lane's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += v;
     }
-    before -= mine;
+    const long long total = __shfl_sync(0xffffffffu, sums, 31), below = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+    before += (warp ? below : 0) - mine;
     const int n_runs = (int)min((long long)k.clusters, (total + kMinRun - 1) / kMinRun);
-    const long long lo = n_runs ? total * cluster / n_runs : 0, hi = n_runs ? total * (cluster + 1) / n_runs : 0;
+    long long lo = 0, hi = 0;
+    if (n_runs && total < 0x7fffffffll / kMaxClusters) {           // the common case without 64-bit divisions
+        lo = (uint32_t)total * (uint32_t)cluster / (uint32_t)n_runs;
+        hi = (uint32_t)total * (uint32_t)(cluster + 1) / (uint32_t)n_runs;
+    } else if (n_runs) {
+        lo = total * cluster / n_runs;
+        hi = total * (cluster + 1) / n_runs;
+    }
     const bool busy = cluster < n_runs;
     if (busy && before <= lo && lo < before + mine) {              // one thread: the run starts among its units
         long long at = before;
@@ -538,14 +547,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     for (int c = 0; c < 32; ++c) w[c] = up2(w[c]);
                 tc::tmem_st32(tmem + kQCol + at * 32 + lane_off, w);
             }
-            // The other atoms keep their swizzle: bytes move as they are, a quarter of a row per thread.
+            // The other atoms keep their swizzle: bytes move as they are, a quarter of a row per thread (rows side by side at different
+            // chunks: other banks).
 #pragma unroll
             for (int at = kQTmem; at < kAtoms; ++at)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint4 v = *reinterpret_cast<const uint4*>(src + at * kQAtom + (4 * hf + 2 * wg + c) * 16);
+                    uint4 v = *reinterpret_cast<const uint4*>(src + at * kQAtom + ((4 * hf + 2 * wg + c ^ row & 7) << 4));
                     if constexpr (FP8) v = make_uint4(up2(v.x), up2(v.y), up2(v.z), up2(v.w));
-                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + (4 * hf + 2 * wg + c) * 16) = v;
+                    *reinterpret_cast<uint4*>(sm.q[at - kQTmem] + row * 128 + ((4 * hf + 2 * wg + c ^ row & 7) << 4)) = v;
                 }
             tc::fence_proxy_async_smem();
             tc::tmem_wait_st();
