@@ -6,8 +6,8 @@
 //
 // Units and cut.  The rows of a group (q_group tokens x H heads, one sequence) are taken 128 at a time: a unit,
 // whose work is ceil(longest context of its tokens / 64) key tiles.  The tiles of all units, laid end to end, are
-// cut into equal runs, one per cluster, so ragged lengths and few tokens load the GPU evenly.  A unit that lies
-// in one run is written out; one that is cut leaves FP32 partial results (at most two per cluster), joined by
+// cut into equal runs, one per cluster, so ragged lengths and few tokens load the GPU evenly (few units are cut each by
+// itself where that costs little).  A unit that lies in one run is written out; one that is cut leaves FP32 partial results (at most two per cluster), joined by
 // latent_merge_kernel.  The cut depends on the inputs only, so results repeat bit for bit.
 //
 // A cluster is two CTAs and one tcgen05 pair (cta_group::2, M = 128): CTA c holds rows [64 c, 64 c + 64) of the
@@ -62,6 +62,7 @@ constexpr int kSCol = 256, kQCol = 320;
 constexpr int kSegs = 3;                                         // published segments
 constexpr int kMaxClusters = 80;
 constexpr int kMinRun = 2;                       // key tiles of a run at least: a shorter one costs more to join than it saves
+constexpr int kSpare = 5;                        // key tiles that a run may be longer to lie in one unit
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8;
 // The other warps.  FP8 (24 warps): the four schedulers (warp mod 4) share the widening evenly, the MMAs' with less of it.
 template <bool FP8> constexpr int kPlanWarp = FP8 ? 21 : 9;
@@ -84,7 +85,10 @@ struct Smem {
     float m_last[2][kRows];                      // each warpgroup's last reference, and its sums by half
     union {
         float l_last[2][128];
-        long long scan[32];                      // the plan's warp sums, before any tile
+        struct {                                 // the plan's, before any tile
+            long long scan[32];                  // sums of the warps
+            int tiles[kMaxClusters];             // of each unit, where there are no more units than clusters
+        } plan;
     };
     Seg seg[kSegs];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -313,9 +317,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         const long long v = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += v;
     }
-    if (lane == 31) sm.scan[warp] = before;
+    if (lane == 31) sm.plan.scan[warp] = before;
+    if (k.units <= k.clusters && threadIdx.x < k.units) sm.plan.tiles[threadIdx.x] = (int)mine;
     __syncthreads();
-    long long sums = lane < kThreads / 32 ? sm.scan[lane] : 0;     // of the warps up to this lane's
+    long long sums = lane < kThreads / 32 ? sm.plan.scan[lane] : 0;     // of the warps up to this lane's
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, sums, o);
@@ -323,11 +328,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     }
     const long long total = __shfl_sync(0xffffffffu, sums, 31), below = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
     before += (warp ? below : 0) - mine;
-    const int n_runs = (int)min((long long)k.clusters, (total + kMinRun - 1) / kMinRun);
+    int n_runs = (int)min((long long)k.clusters, (total + kMinRun - 1) / kMinRun);
     long long lo = 0, hi = 0;
     if (n_runs && total < 0x7fffffffll / kMaxClusters) {           // the common case without 64-bit divisions
         lo = (uint32_t)total * (uint32_t)cluster / (uint32_t)n_runs;
         hi = (uint32_t)total * (uint32_t)(cluster + 1) / (uint32_t)n_runs;
+        // A run with parts of two units pays for the second's start, about as much as kSpare tiles: where runs up to so
+        // much longer suffice, every unit is cut by itself, evenly (4 tokens at 1000 rows 24.9 -> 21.1 us, 4 verify tokens of 128
+        // heads at 4000 rows 34 -> 28; with 10 tiles to spare some longer contexts lose 5%).
+        if (k.units > 1 && k.units <= n_runs) {
+            int t[3], len = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) t[i] = i * 32 + lane < k.units ? sm.plan.tiles[i * 32 + lane] : 0;
+            const int even = ((int)total + n_runs - 1) / n_runs;
+            for (int l = even; l <= even + kSpare && !len; ++l) {
+                int runs = 0;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) runs += (t[i] + l - 1) / l;
+                if ((int)__reduce_add_sync(0xffffffffu, runs) <= n_runs) len = l;
+            }
+            if (len) {
+                int r0 = 0, t0 = 0;              // runs and tiles of the units before
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (i * 32 >= k.units) break;
+                    const int runs = (t[i] + len - 1) / len;
+                    int r = runs, n = t[i];
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int rv = __shfl_up_sync(0xffffffffu, r, o), nv = __shfl_up_sync(0xffffffffu, n, o);
+                        if (lane >= o) { r += rv; n += nv; }
+                    }
+                    const int j = cluster - (r0 + r - runs);       // of this lane's unit
+                    const unsigned mine_is = __ballot_sync(0xffffffffu, j >= 0 && j < runs);
+                    if (mine_is) {
+                        const uint32_t d = max(runs, 1);
+                        const int from = t0 + n - t[i] + (int)((uint32_t)t[i] * (uint32_t)j / d);
+                        const int to = t0 + n - t[i] + (int)((uint32_t)t[i] * (uint32_t)(j + 1) / d);
+                        lo = __shfl_sync(0xffffffffu, from, __ffs(mine_is) - 1);
+                        hi = __shfl_sync(0xffffffffu, to, __ffs(mine_is) - 1);
+                    }
+                    r0 += __shfl_sync(0xffffffffu, r, 31);
+                    t0 += __shfl_sync(0xffffffffu, n, 31);
+                }
+                n_runs = r0;
+            }
+        }
     } else if (n_runs) {
         lo = total * cluster / n_runs;
         hi = total * (cluster + 1) / n_runs;

@@ -606,6 +606,19 @@ def test_latent_units_of_many_parts(cuda, fp8, H, lens):
         s.check()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,lens,G", [(128, [700, 64, 1, 2000], 1), (128, [4000], 4), (64, [65, 129, 1500, 30, 700, 64, 128, 1], 2),
+                                      (128, [300 + 17 * i for i in range(33)], 1), (16, [40] * 70, 1), (128, [100, 5000] * 20, 1)])
+def test_latent_units_cut_apart(cuda, fp8, H, lens, G):
+    """Up to as many units as clusters, of even and uneven lengths, one token of padding among them."""
+    pos = [list(p) for p in _tail([max(n, G) for n in lens], G)]
+    if len(lens) > 3:
+        pos[2] = [-1] * G
+    s = Latent(len(lens) + H + G, H, [max(n, G) for n in lens], pos, fp8=fp8)
+    s.run()
+    s.check()
+
+
 def test_first_calls_of_a_process_are_captured(cuda):
     """A process whose first calls are captured replays them."""
     import subprocess
