@@ -34,7 +34,7 @@
 //
 // Measured: 32 tokens of 128 heads at 32K-64K rows 400 us (1.1 PFLOP/s, 4.6 TB/s; a tile of 64 keys takes 1,470 cycles, 1,244
 // of them products, at 1.4-1.6 GHz under the power limit), FP8 450 us (2,400 cycles: widening); a 500-token chunk behind 15.5K
-// rows 1.3 ms, 1.26 PFLOP/s; one token at 1000 rows 17.6 us, all latency.
+// rows 1.3 ms, 1.26 PFLOP/s; one token at 1000 rows 16.3 us, all latency.
 #include <cmath>
 #include <cstring>
 #include <mutex>
