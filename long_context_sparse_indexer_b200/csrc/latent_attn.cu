@@ -34,7 +34,7 @@
 //
 // Measured: 32 tokens of 128 heads at 32K-64K rows 400 us (1.1 PFLOP/s, 4.6 TB/s; a tile of 64 keys takes 1,470 cycles, 1,244
 // of them products, at 1.4-1.6 GHz under the power limit), FP8 450 us (2,400 cycles: widening); a 500-token chunk behind 15.5K
-// rows 1.3 ms, 1.26 PFLOP/s; one token at 1000 rows 16.3 us, all latency.
+// rows 1.3 ms, 1.26 PFLOP/s; one token at 1000 rows 15.9 us, all latency.
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -1066,8 +1066,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     }
 }
 
-// Joins the partial results of the units that a run's start cuts.  Block (c, y): run c + 1's first unit, when that run
-// is the first to start inside it; a CTA's rows and 4 V dims of each half-row.  Thread = lane of the partial results, in
+// Joins the partial results of the units that a run's start cuts.  Block (x, y): with one group (P = 1) run x + 1's first
+// unit, when that run is the first to start inside it, else unit x; a CTA's rows and 4 V dims of each half-row.  Thread = lane of the partial results, in
 // one of P groups; a group takes every P-th part in key order with weights exp(lse - its own maximum), and the groups'
 // results are joined in order the same way.  Launched while the attention still runs: it waits for its end.
 template <int V, int P>
@@ -1080,13 +1080,29 @@ __global__ void __launch_bounds__(128 * P) latent_merge_kernel(const __grid_cons
     __shared__ float2 stat_s[P > 1 ? P - 1 : 1][P > 1 ? 128 : 1];
     WsHeader* w = &sh;
     for (int i = threadIdx.x; i < kMaxClusters; i += blockDim.x) { w->unit[i] = ws->unit[i]; w->k0[i] = ws->k0[i]; }
-    const int c = blockIdx.x + 1, n_runs = ws->clusters;
-    __syncthreads();
-    if (c >= n_runs || w->k0[c] == 0) return;
-    const int u = w->unit[c];
-    if (w->unit[c - 1] == u && w->k0[c - 1] > 0) return;           // an earlier run is the first
-    int last = c;
-    while (last + 1 < n_runs && w->unit[last + 1] == u) ++last;    // every later run of the unit starts inside it
+    const int n_runs = ws->clusters;
+    int c, u, last;                              // runs c .. last start inside unit u
+    if constexpr (P == 1) {
+        c = blockIdx.x + 1;
+        __syncthreads();
+        if (c >= n_runs || w->k0[c] == 0) return;
+        u = w->unit[c];
+        if (w->unit[c - 1] == u && w->k0[c - 1] > 0) return;       // an earlier run is the first
+        last = c;
+        while (last + 1 < n_runs && w->unit[last + 1] == u) ++last;
+    } else {
+        __shared__ int first;
+        u = blockIdx.x;
+        if (threadIdx.x == 0) first = kMaxClusters;
+        __syncthreads();
+        const int i = threadIdx.x;
+        const bool in = i < n_runs && w->unit[i] == u && w->k0[i] > 0;
+        if (in) atomicMin(&first, i);
+        const int n_in = __syncthreads_count(in);
+        if (n_in == 0) return;
+        c = first;
+        last = c + n_in - 1;
+    }
     constexpr int kSlices = 64 / V;
     const int rank = blockIdx.y / kSlices, c4 = (blockIdx.y % kSlices) * V;
     const int L = threadIdx.x & 127, part = threadIdx.x >> 7, row = L & 63;
@@ -1211,9 +1227,10 @@ cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtenso
     cudaLaunchConfig_t cfg{};
     // Units of eight parts and more: four groups of a block share them.  Units of few: small blocks that wait resident
     // beside the attention (12 units of 6 parts 45.9 us so, 50.4 in groups; one token at 48752 rows, 74 parts, 46.4 us in
-    // groups and 73 in one).
+    // groups and 73 in one).  The large blocks are few, units x 64: they cannot wait beside the attention, and one set per
+    // run, most of it leaving at once, took 31.5 instead of 26.4 us for one token at 27,000 rows.
     const bool wide = k.units * 8 <= k.clusters;
-    cfg.gridDim = dim3(k.clusters - 1, wide ? 64 : 32);
+    cfg.gridDim = dim3(wide ? k.units : k.clusters - 1, wide ? 64 : 32);
     cfg.blockDim = dim3(wide ? 512 : 128);
     cfg.stream = st;
     cudaLaunchAttribute at{};
