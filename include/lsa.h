@@ -337,7 +337,8 @@ lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x,
  * (q_group) belong to one sequence, that of the group's first token, and read its rows together.  A token
  * with q_pos[t] < 0 is padding: o = 0, lse = -inf.  A position or a sequence outside the batch is reported
  * and its token treated as padding.  Cached values at rows 0 .. the group's largest q_pos must be finite;
- * what lies behind them may be anything.  With an FP8 cache |q| < 2^67 and scale * sm_scale < 2^58.
+ * what lies behind them may be anything.  A query with a NaN or an infinity gives NaN (o and lse).
+ * With an FP8 cache |q| < 2^67 and scale * sm_scale < 2^58.
  *   q [T][H][576] BF16; o [T][H][512] of out_dtype (LSA_BF16, or LSA_FP32 for results that are merged later
  *   with lsa_merge_partials); lse [T][H] float or NULL.  1 <= H <= 1024, q_group * H < 2^31 / 1024.
  *   The work is cut evenly over the GPU by rows read, so ragged lengths need no split count; partial
@@ -359,7 +360,8 @@ size_t lsa_latent_attn_workspace_size(int T, int q_group, int H);
  * beyond it are reported and not computed; 0: the call does nothing).  Strides in elements, rows 16-byte aligned:
  *   q [T][H][192], k_nope [S][H][128], v [S][H][128], k_rope [S][64], all BF16 -- k_nope and v may be the
  *   halves of one [S][H][256] projection; o [T][H][128] contiguous, of out_dtype (LSA_BF16 or LSA_FP32);
- *   lse [T][H] float or NULL.  Keys and values of a sequence must be finite. */
+ *   lse [T][H] float or NULL.  Keys and values of a sequence must be finite; a query with a NaN or an infinity
+ *   that sees a key gives NaN (o and lse). */
 lsa_status lsa_latent_attn_expanded(int B, int T, int S, int H, int max_q, const int32_t* q_start,
                                     const int32_t* k_start, const void* q, int64_t q_tok_stride,
                                     int64_t q_head_stride, const void* k_nope, int64_t k_tok_stride,

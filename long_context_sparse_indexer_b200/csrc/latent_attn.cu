@@ -657,7 +657,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (!alive) break;
                 const float m0 = sm.m_last[0][row], m1 = sm.m_last[1][row];
                 m = fmaxf(m0, m1);
-                l = (m0 == kNegInf ? 0.f : sm.l_last[0][L] * ex2(m0 - m)) + (m1 == kNegInf ? 0.f : sm.l_last[1][L] * ex2(m1 - m));
+                // No reference yet: the sum is 0, or NaN.
+                l = (m0 == kNegInf ? sm.l_last[0][L] : sm.l_last[0][L] * ex2(m0 - m)) +
+                    (m1 == kNegInf ? sm.l_last[1][L] : sm.l_last[1][L] * ex2(m1 - m));
                 l += swap(l);                        // x + y = y + x: both halves hold the same sum
             }
             if (have) take_q(r);
@@ -667,8 +669,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     alive = alive && __all_sync(0xffffffffu, wait(&sm.pv_done[j & 1], (j >> 1) & 1, abort_flag));
                 if (!alive) break;
                 tc::tc_fence_after();
-                const float inv = l > 0.f ? (FP8 ? kUp / a.sm_scale_log2 : 1.f) / l : 0.f;
-                const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
+                // A sum of 0 means that the row saw no key; NaN (a query that is not finite) stays NaN.
+                const float inv = l == 0.f ? 0.f : (FP8 ? kUp / a.sm_scale_log2 : 1.f) / l;
+                const float lse = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994530942f;
                 const bool whole = cur.k0 == 0 && cur.k1 == cur.n;
                 const int slot = 2 * cluster + (cur.k0 == 0 ? 1 : 0);
                 const bool write = grow < k.group_rows;
@@ -686,7 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     tc::tmem_wait_ld();
                     float f[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                    for (int e = 0; e < 32; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(ov[e]) * inv;
                     if (!whole) {                // lanes side by side
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -796,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     if (lane == 0) tc::mbar_arrive(&sm.hand[wg][quarter]);
                 }
                 if (m_new != m) {                // this warpgroup's sum to the new reference
-                    l = m == kNegInf ? 0.f : l * ex2(m - m_new);
+                    if (m != kNegInf) l *= ex2(m - m_new);
                     m = m_new;
                 }
                 const float mref = m == kNegInf ? 0.f : m;
@@ -862,6 +865,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 __syncwarp();
                 if (lane == 0) arrive0(&sm.p_full[wg]);
             }
+            // Keys seen, but every score -inf (an infinite query): no reference came of the segment's first tile.
+            if (wg == (tile & 1) && m == kNegInf && lim > s.k0 * kTile) l = __int_as_float(0x7fc00000);
             // The stages' parities move on for the tiles of both warpgroups.
             if (n / kStages & 1) stage_ph ^= (1u << kStages) - 1;
             for (int i = n - n % kStages; i < n; ++i) stage_ph ^= 1u << ((r + i) % kStages);
@@ -1159,7 +1164,7 @@ __global__ void __launch_bounds__(128 * P) latent_merge_kernel(const __grid_cons
         m = mm;
     }
     if (!live) return;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;                // 0: no key in any part
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
     const size_t orow = (size_t)g * k.group_rows + grow, at = orow * kDv + (L >> 6) * 256 + c4 * 4;
@@ -1173,7 +1178,7 @@ __global__ void __launch_bounds__(128 * P) latent_merge_kernel(const __grid_cons
                 make_uint4(pack_bf16x2(acc[e].x, acc[e].y), pack_bf16x2(acc[e].z, acc[e].w),
                            pack_bf16x2(acc[e + 1].x, acc[e + 1].y), pack_bf16x2(acc[e + 1].z, acc[e + 1].w));
     }
-    if (L < kRows && c4 == 0 && a.lse) a.lse[orow] = sum > 0.f ? m + logf(sum) : kNegInf;
+    if (L < kRows && c4 == 0 && a.lse) a.lse[orow] = sum == 0.f ? kNegInf : m + logf(sum);
 }
 
 // The cache as (64 dims, rows, 9 chunks of dims, pages), box 64 x 8 x `chunks` x 1; BF16 under the 128-byte swizzle, codes plain.

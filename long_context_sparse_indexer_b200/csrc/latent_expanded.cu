@@ -452,7 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++outs;
             }
             tc::tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            // Zero for a row that sees no key; with keys every finite row has a positive sum, and a query that is not finite
+            // gives NaN.
+            const bool none = lim <= 0;
+            if (!none && !(l > 0.f)) l = __int_as_float(0x7fc00000);
+            const float inv = 1.f / l;
             const size_t orow = (size_t)(p.q0 + t * kM + row) * a.H + p.h;
 #pragma unroll 1
             for (int c = 0; c < kDv / 32; ++c) {
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (live) {
                     float f[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(ov[e]) * inv : 0.f;
+                    for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(ov[e]) * inv;
                     if (a.o_f32) {
                         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * kDv + c * 32);
 #pragma unroll
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (live && a.lse) a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : kNegInf;
+            if (live && a.lse) a.lse[orow] = none ? kNegInf : (m + log2f(l)) * 0.69314718055994530942f;
             tc::tc_fence_before();                   // the next item's first product overwrites O after this warp's p_full
         }
     }

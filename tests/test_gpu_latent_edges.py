@@ -1,0 +1,78 @@
+"""Rotation, cache append and latent attention where a call's meaning has an edge: values that are not finite, rows marked
+bad, pages that share their rows, results joined over shards, prompts of very different lengths."""
+import math
+
+import pytest
+import torch
+
+from long_context_sparse_indexer_b200 import lsa
+
+from .test_gpu_latent_ops import DEV, Expanded, Latent, _close, _gen, _ints, _latent_reference, _normal, _status, _tail
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = math.inf, math.nan
+
+
+# ------------------------------------------------------------------ queries that are not finite
+
+# What a query row holds: one NaN; one infinity (scores of both signs); an infinity against a key dimension of one
+# sign, so that every score is -inf or every score +inf.  The softmax is NaN for each.
+QUERIES = ["nan", "inf", "all_minus", "all_plus"]
+
+
+def _spoil(row, kind):
+    if kind in ("nan", "inf"):
+        row[5] = NAN if kind == "nan" else INF
+    else:
+        row[-1] = INF if kind == "all_minus" else -INF
+
+
+@pytest.mark.parametrize("kind", QUERIES)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,lens,G,f32", [(128, [700, 64, 1], 1, False), (16, [300, 40], 4, True), (128, [30000], 1, False),
+                                          (64, [20000], 2, True), (128, [4000 + 7 * i for i in range(12)], 1, True)])
+def test_latent_query_that_is_not_finite(cuda, kind, fp8, H, lens, G, f32):
+    """o and lse of its row are NaN, in one run or joined from many; every other row keeps its bits; padding stays zero."""
+    pos = _tail(lens, G)
+    if G > 1:
+        pos[0][0] = -1                                               # padding, spoiled too
+    s = Latent(H + len(lens), H, lens, pos, fp8=fp8, f32=f32, scale=0.5)
+    s.cache.data[..., 575] = 0xb8 if fp8 else -1.0                   # e4m3 -1
+    s.run()
+    o, lse = s.o.clone(), s.lse.clone()
+    assert o.isfinite().all()
+    T = len(lens) * G
+    rows = sorted({(0, 0), (0, H - 1), (T - 1, H // 2), (T // 2, H // 3)})
+    for t, h in rows:
+        _spoil(s.q[t, h], kind)
+    s.run()
+    assert lsa.read_device_status(s.st) == lsa.OK
+    for t, h in rows:
+        if pos[t // G][t % G] < 0:
+            continue
+        assert s.o[t, h].isnan().all() and s.lse[t, h].isnan(), (t, h)
+        s.o[t, h], s.lse[t, h] = o[t, h], lse[t, h]
+    assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
+
+
+@pytest.mark.parametrize("kind", QUERIES)
+@pytest.mark.parametrize("causal,f32", [(True, False), (False, True)])
+def test_expanded_query_that_is_not_finite(cuda, kind, causal, f32):
+    """As above; a query that sees no key gives zero and -inf whatever it holds."""
+    s = Expanded(8, 3, [300, 40], [500, 7], causal=causal, f32=f32)
+    s.kr[:, 63] = -1.0
+    s.run()
+    o, lse = s.o.clone(), s.lse.clone()
+    rows = [(0, 0), (130, 2), (299, 1), (300, 0), (339, 2)]          # 300: 33 keys short of its first, when causal
+    for t, h in rows:
+        _spoil(s.q[t, h], kind)
+    s.run()
+    assert lsa.read_device_status(s.st) == lsa.OK
+    for t, h in rows:
+        if causal and t == 300:
+            assert (s.o[t, h] == 0).all() and s.lse[t, h] == -INF
+            continue
+        assert s.o[t, h].isnan().all() and s.lse[t, h].isnan(), (t, h)
+        s.o[t, h], s.lse[t, h] = o[t, h], lse[t, h]
+    assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
