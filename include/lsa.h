@@ -244,7 +244,7 @@ lsa_status lsa_sparse_attn_partial(const lsa_batch* batch, const void* q, int H,
 /* Log-sum-exp merge of n_parts partial attentions over disjoint row sets, in part order:
  * with m = max_p lse_p and w_p = exp(lse_p - m), o = sum_p (w_p / sum w) o_p and
  * lse = m + log(sum w); a part with lse = -inf (no rows) contributes nothing, and all parts
- * empty give o = 0, lse = -inf.  o_parts [n_parts][T][H][Dv] float, lse_parts [n_parts][T][H]
+ * empty give o = 0, lse = -inf; a part with lse = NaN makes both NaN.  o_parts [n_parts][T][H][Dv] float, lse_parts [n_parts][T][H]
  * float, o [T][H][Dv] BF16 (rounded to nearest even), lse [T][H] float or NULL.  Dv a multiple of
  * 8, 16-byte aligned o_parts and o; 1 <= n_parts <= 1024. */
 lsa_status lsa_merge_partials(const float* o_parts, const float* lse_parts, int n_parts, int T, int H, int Dv,

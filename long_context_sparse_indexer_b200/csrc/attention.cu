@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const float* part_
     }
     const float l = lane < n_split ? __ldcg(part_lse + row0 + (size_t)lane * part_stride) : kNegInf;
     const float m = warp_max(l);
-    const float e = lane < n_split && m != kNegInf ? expf(l - m) : 0.f;
+    const float e = l == kNegInf ? 0.f : expf(l - m);              // NaN (which the maximum leaves out) stays NaN
     float wsum = 0.f;
     for (int s = 0; s < n_split; ++s) wsum += __shfl_sync(0xffffffffu, e, s);
     const float rs = wsum > 0.f ? 1.f / wsum : 0.f;
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const float* part_
         if (act) axpy4(ws, __ldcg(src(s)), acc);
     }
     if (act) merge_store(acc, ((size_t)t * H + h) * DV + d, o, o32);
-    if (lse && lane == 0 && (gw % chunks) == 0) lse[(size_t)t * H + h] = wsum > 0.f ? m + logf(wsum) : kNegInf;
+    if (lse && lane == 0 && (gw % chunks) == 0) lse[(size_t)t * H + h] = wsum == 0.f ? kNegInf : m + logf(wsum);
 }
 
 // More than 32 splits: block = one (token, head), thread = 4 consecutive V dims (and every 512th
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_wide_kernel(const float* 
     __syncthreads();
     float m = kNegInf, wsum = 0.f;
     for (int s = 0; s < n_split; ++s) m = fmaxf(m, s_l[s]);
-    for (int s = 0; s < n_split; ++s) wsum += m == kNegInf ? 0.f : expf(s_l[s] - m);
+    for (int s = 0; s < n_split; ++s) wsum += s_l[s] == kNegInf ? 0.f : expf(s_l[s] - m);       // NaN stays NaN
     const float rs = wsum > 0.f ? 1.f / wsum : 0.f;
     for (int d = 4 * threadIdx.x; d < DV; d += 4 * kMergeThreads) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -375,11 +375,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_wide_kernel(const float* 
                     x[u] = __ldcg(reinterpret_cast<const float4*>(part_o + (row0 + (size_t)(s0 + u) * part_stride) * DV + d));
 #pragma unroll
             for (int u = 0; u < kMergeNS; ++u)
-                if (s0 + u < n_split) axpy4((m == kNegInf ? 0.f : expf(s_l[s0 + u] - m)) * rs, x[u], acc);
+                if (s0 + u < n_split) axpy4((s_l[s0 + u] == kNegInf ? 0.f : expf(s_l[s0 + u] - m)) * rs, x[u], acc);
         }
         merge_store(acc, ((size_t)t * H + h) * DV + d, o, o32);
     }
-    if (lse && threadIdx.x == 0) lse[(size_t)t * H + h] = wsum > 0.f ? m + logf(wsum) : kNegInf;
+    if (lse && threadIdx.x == 0) lse[(size_t)t * H + h] = wsum == 0.f ? kNegInf : m + logf(wsum);
 }
 
 cudaError_t launch_merge_partials(const float* part_o, const float* part_lse, int n_part, int64_t part_stride,

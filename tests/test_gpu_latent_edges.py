@@ -76,3 +76,23 @@ def test_expanded_query_that_is_not_finite(cuda, kind, causal, f32):
         assert s.o[t, h].isnan().all() and s.lse[t, h].isnan(), (t, h)
         s.o[t, h], s.lse[t, h] = o[t, h], lse[t, h]
     assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
+
+
+# ------------------------------------------------------------------ joined results
+
+@pytest.mark.parametrize("R", [1, 3, 30, 40])
+def test_merge_of_parts_that_are_not_finite(cuda, R):
+    """A part whose lse is NaN makes the joined o and lse NaN, alone or among others; the other rows keep their bits."""
+    g = _gen(R)
+    o_parts, l_parts = _normal(g, R, 2, 5, 512, dtype=torch.float32), _normal(g, R, 2, 5, dtype=torch.float32)
+    o, lse = torch.empty(2, 5, 512, dtype=torch.bfloat16, device=DEV), torch.empty(2, 5, device=DEV)
+    lsa.merge_partials(o_parts, l_parts, o, lse)
+    want, wl = o.clone(), lse.clone()
+    for p, t, h in ((R - 1, 0, 1), (0, 1, 4)):
+        o_parts[p, t, h], l_parts[p, t, h] = NAN, NAN
+    o_parts[:, 1, 2], l_parts[:, 1, 2] = NAN, NAN                    # every part
+    lsa.merge_partials(o_parts, l_parts, o, lse)
+    for t, h in ((0, 1), (1, 4), (1, 2)):
+        assert o[t, h].isnan().all() and lse[t, h].isnan(), (t, h)
+        o[t, h], lse[t, h] = want[t, h], wl[t, h]
+    assert torch.equal(o, want) and torch.equal(lse, wl)
