@@ -970,7 +970,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     if ((tile & 1) != set) continue;
                     ok = __all_sync(0xffffffffu, wait(&sm.code_full[st], turn, abort_flag));
                     if (!ok) break;
+                    // A row whose codes are NaN (stored so by the append for a row with a NaN or an infinity; widening moves
+                    // bits and would make them numbers) gets a NaN among its rotary dims, which only the scores read.
+                    const bool bad = (sm.ring[st][src + (kAtoms - 1) * (kAtom / 2)] & 0x7f) == 0x7f;
                     widen(sm.ring[st] + src, sm.ring[st] + dst, kAtoms);
+                    if (bad) *reinterpret_cast<uint32_t*>(sm.ring[st] + dst + (kAtoms - 1) * kAtom) = 0x7fc07fc0u;
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive0(&sm.k_full[st]);

@@ -96,3 +96,38 @@ def test_merge_of_parts_that_are_not_finite(cuda, R):
         assert o[t, h].isnan().all() and lse[t, h].isnan(), (t, h)
         o[t, h], lse[t, h] = want[t, h], wl[t, h]
     assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+# ------------------------------------------------------------------ rows marked bad
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("G", [1, 3])
+def test_tokens_that_see_a_bad_row(cuda, fp8, bad, G):
+    """A row that the append reports (a NaN or an infinity in it) makes the attention of every token that sees it NaN;
+    tokens of groups that end before it are not touched."""
+    g = _gen(17)
+    L, H, at = 300, 20, 130
+    data = torch.zeros(1, L, 576, dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV)
+    cache, st = lsa.Cache(data, torch.zeros(1, L, device=DEV) if fp8 else None), _status()
+    x = _normal(g, L, 576)
+    x[at, 7] = bad
+    pos = torch.arange(L, device=DEV, dtype=torch.int32)
+    zero = torch.zeros(L, dtype=torch.int32, device=DEV)
+    lsa.cache_append(lsa.Batch(_ints(L), zero, pos, L), x, cache, dev_status=st)
+    assert lsa.read_device_status(st) == lsa.ERR_DEVICE_DATA
+    T = 8 * G
+    p = torch.tensor([4, 77, 120, at - 1, at, at + 1, 200, L - 1], device=DEV, dtype=torch.int32)
+    p = (p[:, None] - torch.arange(G, device=DEV, dtype=torch.int32).flip(0)).reshape(-1).contiguous()
+    q = _normal(g, T, H, 576)
+    q[..., 7] = q[..., 7].abs() + 0.5                                # the infinity's score is +inf
+    o, lse = torch.empty(T, H, 512, dtype=torch.bfloat16, device=DEV), torch.empty(T, H, device=DEV)
+    ws, st = torch.empty(lsa.latent_attn_workspace_size(T, G, H), dtype=torch.uint8, device=DEV), _status()
+    lsa.latent_attn(lsa.Batch(_ints(L), zero[:T], p, L, q_group=G), q, cache, 1 / 24, o, lse, ws=ws, dev_status=st)
+    assert lsa.read_device_status(st) == lsa.OK
+    rows = data[0].view(torch.float8_e4m3fn).double() * cache.scale[0].double()[:, None] if fp8 else data[0].double()
+    for t in range(T):
+        if int(p[t]) >= at:
+            assert o[t].isnan().all() and lse[t].isnan().all(), t
+        elif fp8 or int(p[t // G * G + G - 1]) < at:
+            _close(o[t], lse[t], _latent_reference(q[t], rows, int(p[t]) + 1, 1 / 24), 576, t)
