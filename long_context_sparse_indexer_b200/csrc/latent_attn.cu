@@ -891,8 +891,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 *in_page = 0;
                 if (base + lane / 4 >= n || key >= s.len) return a.n_pages;        // outside the map: zeros
                 const int pg = page_of(a, s.seq, key, in_page);
-                // Sequences that share their rows (stride 0) are one in the map.
-                return pg < 0 ? a.n_pages : (a.table || a.seq_b ? pg : 0);
+                // Sequences or pages that share their rows (stride 0) are one in the map.
+                return pg < 0 ? a.n_pages : (a.seq_b ? pg : 0);
             };
             int nrow, npg = fetch(0, &nrow), crow = 0, cpg = 0;
             for (int i = 0; i < n && ok; ++i, ++r) {
@@ -995,7 +995,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     *row = 0;
                     if (base + lane >= n || key >= s.len) return a.n_pages;        // outside the map: zeros
                     const int pg = page_of(a, s.seq, key, row);
-                    return pg < 0 ? a.n_pages : (a.table || a.seq_b ? pg : 0);
+                    return pg < 0 ? a.n_pages : (a.seq_b ? pg : 0);
                 };
                 int nrow, npg = fetch(0, &nrow), crow = 0, cpg = 0;
                 for (int i = 0; i < n; ++i, ++r, ++tile) {

@@ -131,3 +131,22 @@ def test_tokens_that_see_a_bad_row(cuda, fp8, bad, G):
             assert o[t].isnan().all() and lse[t].isnan().all(), t
         elif fp8 or int(p[t // G * G + G - 1]) < at:
             _close(o[t], lse[t], _latent_reference(q[t], rows, int(p[t]) + 1, 1 / 24), 576, t)
+
+
+# ------------------------------------------------------------------ pages that share their rows
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_latent_pages_on_the_same_rows(cuda, fp8):
+    """A pool whose pages all lie on one page's rows (stride 0): every page holds those rows."""
+    s = Latent(64, 20, [300, 131], _tail([300, 131], 2), page=64, fp8=fp8, bad_pages=False)
+    lead = s.cache.data.shape[0]
+    one = _normal(_gen(65), 1, 64, 576)
+    scale = None
+    if fp8:
+        one = (one.float() * 64).to(torch.float8_e4m3fn).view(torch.uint8)
+        scale = torch.full((1, 64), 1 / 64, device=DEV).expand(lead, -1)
+    s.cache = lsa.Cache(one.expand(lead, -1, -1), scale)
+    rows = one[0].view(torch.float8_e4m3fn).double() / 64 if fp8 else one[0].double()
+    s.rows = rows.repeat(5, 1)[None, :300].expand(2, -1, -1)
+    s.run()
+    s.check()
