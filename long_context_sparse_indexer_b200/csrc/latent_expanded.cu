@@ -121,9 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tc::tmem_alloc(&sm.tmem_base, 512);
     if (threadIdx.x == 9 * 32) {
         tc::prefetch_tmap(&qmap);
-        tc::prefetch_tmap(&kmap);
-        tc::prefetch_tmap(&rmap);
-        tc::prefetch_tmap(&vmap);
+        if (a.S > 0) {                           // without keys the other maps are not encoded, and not touched
+            tc::prefetch_tmap(&kmap);
+            tc::prefetch_tmap(&rmap);
+            tc::prefetch_tmap(&vmap);
+        }
     }
     tc::tc_fence_before();
     __syncthreads();

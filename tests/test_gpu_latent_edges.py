@@ -150,3 +150,29 @@ def test_latent_pages_on_the_same_rows(cuda, fp8):
     s.rows = rows.repeat(5, 1)[None, :300].expand(2, -1, -1)
     s.run()
     s.check()
+
+
+# ------------------------------------------------------------------ sequences without keys, and of very different lengths
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("f32", [False, True])
+def test_expanded_without_any_key(cuda, causal, f32):
+    """No key in the call at all (S = 0): zero and -inf for every query, rows of no sequence left as they were."""
+    s = Expanded(9, 5, [3, 0, 300], [0, 0, 0], causal=causal, f32=f32)
+    s.run()
+    s.check()
+    assert (s.o == 0).all() and (s.lse == -INF).all()
+    s = Expanded(9, 1, [1], [0], causal=causal, f32=f32)
+    s.run()
+    s.check()
+    assert (s.o == 0).all() and (s.lse == -INF).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,nq,nk", [(2, [2500] + [1 + 37 * i % 100 for i in range(40)], [2500] + [1 + 37 * i % 100 for i in range(40)]),
+                                     (20, [1, 900, 3, 1, 64], [3000, 900, 3, 1, 2000])])
+def test_expanded_prompts_of_very_different_lengths(cuda, causal, H, nq, nk):
+    """One long prompt among many short ones: most places of the longest have no counterpart in the others."""
+    s = Expanded(H + len(nq), H, nq, nk, causal=causal)
+    s.run()
+    s.check()
