@@ -543,12 +543,13 @@ const char* lsa_status_string(lsa_status s);
 int         lsa_version(void);
 
 /* Diagnostic: the wall-time limit, in nanoseconds, of the pipeline waits of the tensor-core
- * indexer (lsa_index_score, lsa_index_score_q8, the indexer of lsa_decode_fused) and of the
- * tensor-core block scores, for launches issued after the call; 0 restores the default (2 s).  A
- * CTA whose wait runs out stops its pipeline, waits (with the 2 s bound) for its copies and MMAs
- * in flight, frees its tensor memory and stores LSA_ERR_TIMEOUT in dev_status; its outputs are
- * then incomplete.  A limit shorter than the kernel's own waits makes it give up on purpose: the
- * way to check that path.  Process-wide; returns the previous setting. */
+ * indexer (lsa_index_score, lsa_index_score_q8, the indexer of lsa_decode_fused), of the
+ * tensor-core block scores and of the loading warps of lsa_latent_attn_expanded, for launches
+ * issued after the call; 0 restores the default (2 s).  A CTA whose wait runs out stops its
+ * pipeline, waits (with the 2 s bound) for its copies and MMAs in flight, frees its tensor memory
+ * and stores LSA_ERR_TIMEOUT in dev_status; its outputs are then incomplete.  A limit shorter than
+ * the kernel's own waits makes it give up on purpose: the way to check that path.  Process-wide;
+ * returns the previous setting. */
 uint64_t    lsa_set_wait_limit_ns(uint64_t ns);
 
 #ifdef __cplusplus

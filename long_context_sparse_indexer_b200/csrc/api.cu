@@ -118,7 +118,7 @@ size_t attn_ws(int T, int H, int Dv, int n_split) {
     return align_up((size_t)T * n_split * H * Dv * 4) + align_up((size_t)T * n_split * H * 4);
 }
 
-// Limit of the pipeline waits of the tensor-core indexer and block-score kernels (0: the 2 s
+// Limit of the pipeline waits of the tensor-core indexer, block-score and expanded-attention kernels (0: the 2 s
 // default), set by lsa_set_wait_limit_ns.
 std::atomic<uint64_t> g_wait_limit_ns{0};
 
@@ -464,7 +464,7 @@ lsa_status lsa_latent_attn_expanded(int B, int T, int S, int H, int max_q, const
     a.qt = q_tok_stride; a.qh = q_head_stride; a.kt = k_tok_stride; a.kh = k_head_stride; a.rt = r_tok_stride;
     a.vt = v_tok_stride; a.vh = v_head_stride;
     a.sm_scale_log2 = sm_scale * 1.4426950408889634f; a.causal = causal != 0;
-    a.o = o; a.o_f32 = out_dtype == LSA_FP32; a.lse = lse; a.status = dev_status;
+    a.o = o; a.o_f32 = out_dtype == LSA_FP32; a.lse = lse; a.status = dev_status; a.wait_ns = wait_limit_ns();
     return cuda_status(launch_latent_expanded(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -232,10 +232,11 @@ struct ExpandedArgs {
     int o_f32;
     float* lse;
     int32_t* status;
+    uint64_t wait_ns;            // limit of the loading warps' pipeline waits
 };
 cudaError_t launch_latent_expanded(const ExpandedArgs& a, cudaStream_t st);
 
-// Wait limit the tensor-core indexer and block-score kernels are launched with (api.cu).
+// Wait limit the tensor-core indexer, block-score and expanded-attention kernels are launched with (api.cu).
 uint64_t wait_limit_ns();
 
 // Host-side checks of lsa_sparse_attn's arguments other than its workspace (api.cu).

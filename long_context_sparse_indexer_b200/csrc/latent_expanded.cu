@@ -23,7 +23,8 @@
 // Warps: 0..3 softmax of query tile 0 (thread = row = TMEM lane), 4..7 of tile 1, 8 issues the MMAs, 9 loads keys and
 // values by TMA, 10 clears the rows of a sequence's last key tile that lie behind the sequence (0 x whatever they hold
 // would reach O), 11 takes the blocks, plans them and loads their queries.  All waits are bounded; a CTA that gives up
-// reports LSA_ERR_TIMEOUT.
+// reports LSA_ERR_TIMEOUT.  The waits of warps 9 and 11 take the limit of lsa_set_wait_limit_ns, and every other wait
+// ends with the flag that they set; what is in flight then is waited for with the 2 s bound, each with a flag of its own.
 //
 // Measured: 2048 queries behind 2048 keys, 128 heads, causal: 430 us, 1.2 PFLOP/s under the power limit.  A pair of query tiles
 // takes about 3,700 cycles a key tile where its products take 2,560: the chain score, softmax, product shows.
@@ -77,6 +78,15 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// A wait under a limit, its slow part a call: the roles share the instruction caches (2048 queries behind 2048 keys, 128
+// heads: 444 us with both ways of polling inlined, 428 so).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    return tc::mbar_wait(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    return tc::mbar_test_wait(bar, parity) || wait_slow(bar, parity, abort, limit_ns);
 }
 
 template <int R>
@@ -175,20 +185,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p.n[t] = (end + kN - 1) / kN;
                         }
                         const int d = published % kItems;
-                        ok = tc::mbar_wait(&sm.item_empty[d], ((published / kItems) + 1) & 1, abort_flag);
+                        ok = wait(&sm.item_empty[d], ((published / kItems) + 1) & 1, abort_flag, a.wait_ns);
                         if (!ok) break;
                         sm.item[d] = p;
                         tc::mbar_arrive(&sm.item_full[d]);
                         ++published;
                         if (tiles(p) > 0) {
-                            ok = loaded == 0 || tc::mbar_wait(&sm.q_free, (loaded - 1) & 1, abort_flag);
+                            ok = loaded == 0 || wait(&sm.q_free, (loaded - 1) & 1, abort_flag, a.wait_ns);
                             if (!ok) break;
                             const int hq = a.qh ? h : 0, n_q = p.rows > kM ? 2 : 1;        // a broadcast head has no stride
                             tc::mbar_expect_tx(&sm.q_full, n_q * 3 * kM * 128);
                             for (int t = 0; t < n_q; ++t)
                                 for (int c = 0; c < 3; ++c)
                                     tc::tma_load_3d(sm.q[t][c], &qmap, &sm.q_full, c * 64, hq, p.q0 + t * kM);
-                            ok = tc::mbar_wait(&sm.ask, loaded & 1, abort_flag);
+                            ok = wait(&sm.ask, loaded & 1, abort_flag, a.wait_ns);
                             ++loaded;
                             if (!ok) break;
                         }
@@ -197,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::mbar_expect_tx(&sm.asked, 16);
                     asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
                                  :: "r"(tc::smem_u32(sm.answer)), "r"(tc::smem_u32(&sm.asked)) : "memory");
-                    ok = tc::mbar_wait(&sm.asked, asked & 1, abort_flag);
+                    ok = wait(&sm.asked, asked & 1, abort_flag, a.wait_ns);
                     ++asked;
                     if (!ok) break;
                     const volatile uint64_t* an = reinterpret_cast<const volatile uint64_t*>(sm.answer);
@@ -214,19 +224,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     h = (int)cy;
                     b = (int)cz;
                 }
-                if (ok) ok = tc::mbar_wait(&sm.item_empty[published % kItems], ((published / kItems) + 1) & 1, abort_flag);
+                if (ok) ok = wait(&sm.item_empty[published % kItems], ((published / kItems) + 1) & 1, abort_flag, a.wait_ns);
                 if (ok) {
                     sm.item[published % kItems].more = 0;
                     tc::mbar_arrive(&sm.item_full[published % kItems]);
                 }
-                // No copy outlives the CTA.
-                volatile int drain = 0;
-                if (loaded) tc::mbar_wait(&sm.q_full, (loaded - 1) & 1, &drain);
+                // No copy and no answer outlives the CTA.
+                volatile int drain_q = 0, drain_a = 0;
+                if (loaded) tc::mbar_wait(&sm.q_full, (loaded - 1) & 1, &drain_q);
+                if (asked) tc::mbar_wait(&sm.asked, (asked - 1) & 1, &drain_a);
             }
         } else if (warp == 9) {
             // ---------------- keys and values: the ring's units in the order of their use
             const bool leader = tc::elect_one();
             int u = 0, partials = 0, last[2] = {-kUnits, -kUnits};  // next unit; partial tiles so far, and the units of the latest
+            uint32_t last_ph[2] = {0, 0};        // the phases of v_last that those complete
             bool ok = true;
             while (ok && next_item(p)) {
                 const int n_tiles = tiles(p);
@@ -238,15 +250,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int row = p.k0 + j * kN;
                         for (int c = 0; c < kPerTile; ++c, ++u) {
                             const int s = u % kUnits;
-                            ok = tc::mbar_wait(&sm.empty[s], ((u / kUnits) + 1) & 1, abort_flag);
+                            ok = wait(&sm.empty[s], ((u / kUnits) + 1) & 1, abort_flag, a.wait_ns);
                             uint64_t* bar = &sm.full[s];
                             if (ok && c >= 3 && partial && j == n_tiles - 1) {
                                 // The V units of a partial last tile pass through warp 10, which then completes `full`; it must be
                                 // through with the latest one (unless that unit's place has been used again since).
                                 const int w = last[c - 3];
-                                if (w > u - kUnits && partials > 0) ok = tc::mbar_wait(&sm.full[w % kUnits], (w / kUnits) & 1, abort_flag);
-                                bar = &sm.v_last[c - 3];
-                                last[c - 3] = u;
+                                if (w > u - kUnits && partials > 0) ok = wait(&sm.full[w % kUnits], (w / kUnits) & 1, abort_flag, a.wait_ns);
+                                if (ok) {
+                                    bar = &sm.v_last[c - 3];
+                                    last[c - 3] = u;
+                                    last_ph[c - 3] = partials & 1;
+                                }
                             }
                             if (!ok) break;
                             tc::mbar_expect_tx(bar, kUnitBytes);
@@ -258,19 +273,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (partial) ++partials;
+                    if (partial && ok) ++partials;
                 }
                 ok = __all_sync(0xffffffffu, ok);
             }
             // No copy outlives the CTA: all have landed, at once unless a wait gave up.
-            if (leader) {
-                volatile int drain = 0;
+            if (leader)
                 for (int v = max(0, u - kUnits); v < u; ++v) {
+                    volatile int drain = 0;
                     const int c = v == last[0] ? 0 : (v == last[1] ? 1 : -1);
-                    if (c >= 0 && !ok) tc::mbar_wait(&sm.v_last[c], (partials + 1) & 1, &drain);
+                    if (c >= 0) tc::mbar_wait(&sm.v_last[c], last_ph[c], &drain);      // `full` is warp 10's to complete
                     else tc::mbar_wait(&sm.full[v % kUnits], (v / kUnits) & 1, &drain);
                 }
-            }
         } else if (warp == 8) {
             // ---------------- MMA issuer
             const uint32_t idesc_s = tc::idesc_f16(kM, kN, 1), idesc_o = tc::idesc_f16_bmn(kM, kDv, 1);

@@ -1,6 +1,7 @@
 """Rotation, cache append and latent attention where a call's meaning has an edge: values that are not finite, rows marked
-bad, pages that share their rows, results joined over shards, prompts of very different lengths."""
+bad, pages that share their rows, joined results, prompts of very different lengths, waits that run out."""
 import math
+import time
 
 import pytest
 import torch
@@ -176,3 +177,39 @@ def test_expanded_prompts_of_very_different_lengths(cuda, causal, H, nq, nk):
     s = Expanded(H + len(nq), H, nq, nk, causal=causal)
     s.run()
     s.check()
+
+
+# ------------------------------------------------------------------ a wait that runs out
+
+@pytest.mark.parametrize("H,nq,nk", [(16, [700, 300, 1, 130], [1900, 350, 1, 130]),      # many key tiles, the last of each partial
+                                     (128, [100, 40, 129], [100, 90, 257]),              # one to three, several items a CTA
+                                     (64, [256, 512], [256, 512])])                      # no partial tile
+def test_expanded_gives_up_and_the_context_stays_usable(cuda, H, nq, nk):
+    """With a limit of 1 ns the loading warps give up: the status says so, the launch ends at once (nothing is waited for
+    that cannot come: such a wait would sit out its 2 s), and the next one gives the same bits as before."""
+    s = Expanded(H, H, nq, nk)
+    s.run()
+    s.check()
+    o, lse = s.o.clone(), s.lse.clone()
+    gave_up = 0
+    prev = lsa.set_wait_limit_ns(1)
+    try:
+        for _ in range(5):
+            s.st.zero_()
+            torch.cuda.synchronize()
+            t0 = time.monotonic()
+            s.run()
+            torch.cuda.synchronize()
+            assert time.monotonic() - t0 < 1.0
+            status = lsa.read_device_status(s.st)
+            assert status in (lsa.OK, lsa.ERR_TIMEOUT), lsa.status_string(status)
+            gave_up += status == lsa.ERR_TIMEOUT
+    finally:
+        lsa.set_wait_limit_ns(prev)
+    assert gave_up
+    for _ in range(2):
+        s.st.zero_()
+        s.o.fill_(7.0), s.lse.fill_(7.0)
+        s.run()
+        s.check()
+        assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
