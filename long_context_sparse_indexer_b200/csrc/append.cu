@@ -109,13 +109,13 @@ __global__ void __launch_bounds__(256, SLOTS == 1 ? 4 : 3) append_kernel(const _
             if (ok) {
                 const int len = p.seq_len[b];
                 int64_t lead = b, row = my_pos;
-                int pg = 0;
-                if (p.table) {                   // read under the length, with an index that may be out of the table if it is bad
-                    pg = my_pos / p.page_size;
+                ok = my_pos < len && len <= p.L_alloc;
+                if (p.table && ok) {             // entries behind the last position are not read
+                    const int pg = my_pos / p.page_size;
                     row = my_pos - pg * p.page_size;
-                    lead = my_pos < p.L_alloc ? p.table[b * p.table_ld + pg] : -1;
+                    lead = p.table[b * p.table_ld + pg];
+                    ok = lead >= 0 && lead < p.n_pages;
                 }
-                ok = my_pos < len && len <= p.L_alloc && lead >= 0 && (!p.table || lead < p.n_pages);
                 if (ok) {
                     my_off = lead * p.seq_b + row * p.tok_b;
                     my_sc = lead * p.scale_seq + row;

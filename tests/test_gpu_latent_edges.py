@@ -213,3 +213,22 @@ def test_expanded_gives_up_and_the_context_stays_usable(cuda, H, nq, nk):
         s.run()
         s.check()
         assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
+
+
+# ------------------------------------------------------------------ positions behind a sequence's length
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("entry", [3, -9, 99])
+def test_append_behind_the_length_stores_nothing(cuda, fp8, entry):
+    """A position behind its sequence's length, whatever the page table holds there (a page of the pool or not): reported,
+    no row stored; the tokens beside it are."""
+    table = _ints(0, 1, entry, entry).view(1, 4)
+    data = torch.zeros(5, 8, 128, dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV)
+    scale = torch.zeros(5, 8, device=DEV) if fp8 else None
+    st = _status()
+    x = _normal(_gen(5), 4, 128)
+    lsa.cache_append(lsa.Batch(_ints(12), _ints(0, 0, 0, 0), _ints(11, 12, 16, 31), 32), x, lsa.Cache(data, scale),
+                     pages=lsa.PageTable(table), dev_status=st)
+    assert lsa.read_device_status(st) == lsa.ERR_DEVICE_DATA
+    assert data[1, 3].any() and data.flatten(2).any(-1).sum() == 1
+    assert scale is None or (scale != 0).sum() == 1
