@@ -339,7 +339,8 @@ lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x,
  * and its token treated as padding.  Cached values at rows 0 .. the group's largest q_pos must be finite;
  * what lies behind them may be anything.  A row that lsa_cache_append reported as bad makes the results of
  * the tokens that see it NaN (with a BF16 cache also those of other tokens of their group).  A query with a
- * NaN or an infinity gives NaN (o and lse).  With an FP8 cache |q| < 2^67 and scale * sm_scale < 2^58.
+ * NaN or an infinity gives NaN (o and lse).  With an FP8 cache 2^-30 <= sm_scale <= 2^30 (others are refused),
+ * |q| < 2^67 and scale * sm_scale < 2^58; results that stay below 2^-40 / sm_scale lose accuracy.
  *   q [T][H][576] BF16; o [T][H][512] of out_dtype (LSA_BF16, or LSA_FP32 for results that are merged later
  *   with lsa_merge_partials); lse [T][H] float or NULL.  1 <= H <= 1024, q_group * H < 2^31 / 1024.
  *   The work is cut evenly over the GPU by rows read, so ragged lengths need no split count; partial

@@ -418,6 +418,8 @@ lsa_status lsa_latent_attn(const lsa_batch* batch, const void* q, int H, const l
     if ((s = check_pages(pages, batch)) != LSA_OK) return s;
     if (H < 1 || !(sm_scale > 0.f) || !std::isfinite(sm_scale)) return LSA_ERR_INVALID_ARG;
     if (H > 1024 || (int64_t)batch->q_group * H >= 0x7fffffff / 1024) return LSA_ERR_UNSUPPORTED;
+    // FP8 weights carry 2^60 sm_scale, and the results 2^60 / sm_scale: both in FP32's range.
+    if (kv->dtype == LSA_FP8_E4M3 && (sm_scale < 0x1p-30f || sm_scale > 0x1p30f)) return LSA_ERR_UNSUPPORTED;
     if (out_dtype != LSA_BF16 && out_dtype != LSA_FP32) return LSA_ERR_UNSUPPORTED;
     if (batch->T == 0) return LSA_OK;
     if (!q || !o || !aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3)) return LSA_ERR_INVALID_ARG;
