@@ -232,3 +232,24 @@ def test_append_behind_the_length_stores_nothing(cuda, fp8, entry):
     assert lsa.read_device_status(st) == lsa.ERR_DEVICE_DATA
     assert data[1, 3].any() and data.flatten(2).any(-1).sum() == 1
     assert scale is None or (scale != 0).sum() == 1
+
+
+# ------------------------------------------------------------------ one context over shards
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,L,cuts,G", [(128, 5000, [0, 1700, 1701, 5000], 1), (16, 700, [0, 64, 690, 700], 4), (40, 900, [0, 900], 2)])
+def test_latent_merges_over_shards(cuda, fp8, H, L, cuts, G):
+    """Rows of one context in several caches: 32-bit results over each, merged, are the attention over all of them.  A token
+    that lies before a shard is padding there."""
+    s = Latent(H + L, H, [L], _tail([L], G), page=0, fp8=fp8)
+    n = len(cuts) - 1
+    o, lse = torch.empty(n, G, H, 512, device=DEV), torch.empty(n, G, H, device=DEV)
+    st = _status()
+    for i, (a, e) in enumerate(zip(cuts, cuts[1:])):
+        cache = lsa.Cache(s.cache.data[:, a:e], s.cache.scale[:, a:e] if fp8 else None)
+        pos = torch.where(s.batch.q_pos < a, -1, s.batch.q_pos.clamp(max=e - 1) - a).to(torch.int32)
+        lsa.latent_attn(lsa.Batch(_ints(e - a), s.batch.q_seq, pos, e - a, q_group=G), s.q, cache, s.sm, o[i], lse[i], ws=s.ws,
+                        dev_status=st)
+    assert lsa.read_device_status(st) == lsa.OK
+    lsa.merge_partials(o, lse, s.o, s.lse)
+    s.check()
