@@ -94,7 +94,7 @@ struct Smem {
     uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t k_full[kStages];                    // CTA 0: both CTAs' keys have landed
     uint64_t sc_full[kStages];                   // FP8: kscale is written
-    uint64_t code_full[kStages], x_code[4];      // FP8: the stage's codes have landed; those of exchanged group g
+    uint64_t code_full[2][kStages], x_code[4];   // FP8: the codes of an even / odd tile in the stage have landed; those of exchanged group g
     uint64_t x_go[kStages], x_full[kStages];     // the scores of the stage are done; its exchanged rows have landed
     uint64_t empty[kStages];
     uint64_t q_full, q_ready;                    // queries staged; (CTA 0) moved to their operand places in both CTAs
@@ -272,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sm.k_full[i], FP8 ? kKWarps : 1);     // FP8: four warps of each CTA
             tc::mbar_init(&sm.sc_full[i], 1);
-            tc::mbar_init(&sm.code_full[i], 1);
+            for (int j = 0; j < 2; ++j) tc::mbar_init(&sm.code_full[j][i], 1);
             tc::mbar_init(&sm.x_go[i], 1);
             tc::mbar_init(&sm.x_full[i], FP8 ? kXWarps : 1);
             tc::mbar_init(&sm.empty[i], 1);
@@ -877,7 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         // ---------------- TMA loads.  First warp: queries and own keys (FP8: their codes); second: the exchanged value rows
         const bool xw = warp == kXWarp<FP8>;
         const int my0 = xw ? (rank ^ 1) * kOwn : rank * kOwn;      // first key in a tile of the rows this warp loads
-        int r = 0, seg = 0;
+        int r = 0, tile = 0, seg = 0;
         uint32_t go_ph = 0;
         bool ok = true;
         Seg s;
@@ -895,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 return pg < 0 ? a.n_pages : (a.seq_b ? pg : 0);
             };
             int nrow, npg = fetch(0, &nrow), crow = 0, cpg = 0;
-            for (int i = 0; i < n && ok; ++i, ++r) {
+            for (int i = 0; i < n && ok; ++i, ++r, ++tile) {
                 const int o = i % 8;
                 if (o == 0) {
                     crow = nrow; cpg = npg;
@@ -912,7 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 const uint32_t bar0 = tc::peer_smem(&sm.k_full[st], 0);
                 if (lane == 0) {
                     if (xw) tc::mbar_expect_tx(&sm.x_full[st], kXBytes);
-                    else if (FP8) tc::mbar_expect_tx(&sm.code_full[st], kCodeBytes);
+                    else if (FP8) tc::mbar_expect_tx(&sm.code_full[tile & 1][st], kCodeBytes);
                     else if (rank == 0) tc::mbar_expect_tx(&sm.k_full[st], 2 * kStageBytes);
                 }
                 __syncwarp();
@@ -920,7 +920,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 if (xw) {                        // 256 dims of 8 rows a box
                     if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + (rank ^ 1) * 4 * kAtom, &xmap, &sm.x_full[st], 0, rw, rank * 4, pg);
                 } else if (FP8) {
-                    if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + kCodeAt, &kmap, &sm.code_full[st], 0, rw, 0, pg);
+                    if (lane < 4) tma_load_4d(sm.ring[st] + lane * kGroup + kCodeAt, &kmap, &sm.code_full[tile & 1][st], 0, rw, 0, pg);
                 } else if (lane < 4) {           // 8 rows a box
                     tma_load_4d_pair(sm.ring[st] + lane * kGroup, &kmap, bar0, 0, rw, 0, pg);
                 }
@@ -932,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         // Own keys 0..7: warps 9, 10, 11, 12 and 13, 14, 15, 17; exchanged rows 8..11: 18, 19, 20, 23; scales 12: 22.
         const int w = warp < 16 ? warp - 9 : (warp == 17 ? 7 : (warp == 22 ? 12 : (warp == 23 ? 11 : warp - 10)));
         int r = 0, tile = 0;
-        uint32_t ph = 0;                         // parity of each stage's next phase (codes landed; scores done)
+        uint32_t ph = 0;                         // parity of each stage's next phase (own set's codes landed; scores done)
         bool ok = true;
         Seg s;
         // n atoms of codes at `from` to n atoms at `to` (this lane's 16 codes of each).
@@ -960,16 +960,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             while (ok && next_seg(s)) {
                 r += 2;
                 const int n = s.k1 - s.k0;
-                for (int i = 0; i < n; ++i, ++r, ++tile) {
-                    const int st = r % kStages;
-                    const uint32_t turn = (ph >> st) & 1;
+                for (int i = (tile ^ set) & 1; i < n; i += 2) {
+                    // The stage's barrier of this set: its phases are this set's tiles alone, none of which completes unless the warp
+                    // saw the one before.  (A warp must not wait on what goes on without it: such a phase can be over, and the next
+                    // one too, before it looks, and the parity then says "not yet" for good.)
+                    const int st = (r + i) % kStages;
+                    ok = __all_sync(0xffffffffu, wait(&sm.code_full[set][st], (ph >> st) & 1, abort_flag));
+                    if (!ok) break;
                     ph ^= 1u << st;
-                    // Every tile's stage is waited free for, the other set's too: then no phase of its barriers goes unseen.
-                    ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
-                    if (!ok) break;
-                    if ((tile & 1) != set) continue;
-                    ok = __all_sync(0xffffffffu, wait(&sm.code_full[st], turn, abort_flag));
-                    if (!ok) break;
                     // A row whose codes are NaN (stored so by the append for a row with a NaN or an infinity; widening moves
                     // bits and would make them numbers) gets a NaN among its rotary dims, which only the scores read.
                     const bool bad = (sm.ring[st][src + (kAtoms - 1) * (kAtom / 2)] & 0x7f) == 0x7f;
@@ -979,6 +977,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     __syncwarp();
                     if (lane == 0) arrive0(&sm.k_full[st]);
                 }
+                r += n;
+                tile += n;
             }
         } else if (w < kKWarps + kXWarps) {
             // Warp = 8-row group of the exchanged rows: once the scores have read the dims that they replace, their codes land

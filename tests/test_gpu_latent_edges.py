@@ -253,3 +253,23 @@ def test_latent_merges_over_shards(cuda, fp8, H, L, cuts, G):
     assert lsa.read_device_status(st) == lsa.OK
     lsa.merge_partials(o, lse, s.o, s.lse)
     s.check()
+
+
+# ------------------------------------------------------------------ many short segments
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,B,top", [(96, 86, 12000), (128, 300, 100), (16, 90, 700)])
+def test_latent_segments_of_one_to_a_few_tiles_again_and_again(cuda, fp8, H, B, top):
+    """Contexts from one row up, several a CTA: every wait comes to its end whatever the warps' pace (status OK), the same
+    bits each time."""
+    g = torch.Generator().manual_seed(B)
+    lens = [max(1, int(math.exp(float(torch.rand(1, generator=g)) * math.log(top)))) for _ in range(B)]
+    pos = [[-1] if i % 11 == 3 else [n - 1] for i, n in enumerate(lens)]
+    s = Latent(B, H, lens, pos, page=8, fp8=fp8)
+    s.run()
+    s.check()
+    o, lse = s.o.clone(), s.lse.clone()
+    for _ in range(200):
+        s.run()
+    assert lsa.read_device_status(s.st) == lsa.OK
+    assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
