@@ -932,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         // Own keys 0..7: warps 9, 10, 11, 12 and 13, 14, 15, 17; exchanged rows 8..11: 18, 19, 20, 23; scales 12: 22.
         const int w = warp < 16 ? warp - 9 : (warp == 17 ? 7 : (warp == 22 ? 12 : (warp == 23 ? 11 : warp - 10)));
         int r = 0, tile = 0;
-        uint32_t ph = 0;                         // parity of each stage's next phase (own set's codes landed; scores done)
+        uint32_t ph = 0;                         // parity of each stage's next phase (codes landed, by set; scores done)
         bool ok = true;
         Seg s;
         // n atoms of codes at `from` to n atoms at `to` (this lane's 16 codes of each).
@@ -1020,7 +1020,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
             }
         } else {
-            // Row scales, lane l: keys l and l + 32, loaded a tile ahead.
+            // Row scales, lane l: keys l and l + 32, loaded a tile ahead.  They are put out once the tile's codes have landed: its
+            // stage is free then, and every phase of those barriers is seen (the stage's own has phases of queries between, which
+            // end before the products of the tiles in front of them).
             const float up = kUp * a.sm_scale_log2;
             while (ok && next_seg(s)) {
                 r += 2;
@@ -1046,12 +1048,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     n1 = i < n && o1 >= 0 && lane + 32 < left ? __ldg(a.kv_scale + o1 + lane % 8) : 0.f;
                 };
                 load(0);
-                for (int i = 0; i < n; ++i, ++r) {
+                for (int i = 0; i < n; ++i, ++r, ++tile) {
                     const float s0 = n0, s1 = n1;
                     load(i + 1);
-                    const int st = r % kStages;
-                    ok = __all_sync(0xffffffffu, wait(&sm.empty[st], ((r / kStages) + 1) & 1, abort_flag));
+                    const int st = r % kStages, bit = (tile & 1) * kStages + st;
+                    ok = __all_sync(0xffffffffu, wait(&sm.code_full[tile & 1][st], (ph >> bit) & 1, abort_flag));
                     if (!ok) break;
+                    ph ^= 1u << bit;
                     sm.kscale[st][lane] = s0 * up;
                     sm.kscale[st][32 + lane] = s1 * up;
                     __syncwarp();

@@ -273,3 +273,17 @@ def test_latent_segments_of_one_to_a_few_tiles_again_and_again(cuda, fp8, H, B, 
         s.run()
     assert lsa.read_device_status(s.st) == lsa.OK
     assert torch.equal(s.o, o) and torch.equal(s.lse, lse)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_latent_segments_of_one_then_two_tiles(cuda, f32):
+    """FP8, runs of segments of 3, 9, 1, 1, 2, 1, 1, 1, 2 key tiles and the like, at which the scales once ran ahead of the
+    products and the call timed out."""
+    tiles = [90, 1, 1, 13, 1, 2, 2, 86, 14, 1, 36, 12, 1, 1, 1, 1, 17, 17, 142, 10, 3, 1, 7, 10, 1, 2, 1, 1, 1, 1, 1, 2, 2, 68, 1,
+             14, 1, 45, 1, 2, 12, 3, 1, 37, 1, 80, 1, 2, 1, 1, 18, 2, 12, 1, 140, 9, 1, 1, 2, 1, 1, 1, 140, 181, 2, 1, 1, 33, 1, 1, 2,
+             1, 5, 1, 2, 3, 1, 31, 2, 132, 99, 1, 1, 6]
+    lens = [64 * n - (i * 13) % 64 for i, n in enumerate(tiles)]
+    s = Latent(7, 96, lens, _tail(lens, 1), page=8, fp8=True, f32=f32, wide=True)
+    for _ in range(100):
+        s.run()
+    s.check()
