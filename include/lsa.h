@@ -291,8 +291,9 @@ lsa_status lsa_rope_apply(const lsa_rope* r, int T, int H, int D, int rope_off, 
 /* ---------------------------------------------------------------- paged caches
  * With a page table, a cache is a pool of pages instead of one run of rows per sequence: position p of
  * sequence b is row p % page_size of page table[b * ld + p / page_size], page i starting at
- * data + i * seq_stride (scale + i * scale_seq_stride) -- the lsa_cache's "sequences" are the pages.  Calls
- * that take an lsa_pages accept NULL for a cache without pages.  Entries past a sequence's last position are
+ * data + i * seq_stride (scale + i * scale_seq_stride) -- the lsa_cache's "sequences" are the pages.  The
+ * calls that take an lsa_pages (lsa_cache_append, lsa_latent_attn) accept NULL for a cache without pages; all
+ * others read caches without pages.  Entries past a sequence's last position are
  * never read; an entry that is read and lies outside 0 .. n_pages - 1 is bad device data, and its rows are
  * skipped (lsa_cache_append) or read as zeros (attention). */
 typedef struct {
@@ -314,7 +315,8 @@ typedef struct {
  *   2. with `rope`, elements rope_off .. rope_off + rot_dim - 1 are rotated by q_pos[t];
  *   3. the row is stored as BF16, or as e4m3 codes with scale = max|row| / 448 (1 for a row of zeros),
  *      code = row * (448 / max|row|) rounded to nearest even.
- * All in 32 bits, rounded once (|x| below 2^59 in a normalised part, so that its sum of squares is finite).  A
+ * All in 32 bits, rounded once (|x| below 2^59 in a normalised part, so that its sum of squares is finite, and
+ * its mean square above 2^-100 where eps is 0).  A
  * latent row is [norm_dim = 512 normalised | 64 rotated]; an indexer key is
  * layer-normalised whole and rotated in part.  A token with q_pos[t] < 0 is padding: nothing is stored.
  * A row with a NaN or an infinity is reported (LSA_ERR_DEVICE_DATA) and stored as it is in a BF16 cache, as
@@ -344,8 +346,8 @@ lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x,
  *   q [T][H][576] BF16; o [T][H][512] of out_dtype (LSA_BF16, or LSA_FP32 for results that are merged later
  *   with lsa_merge_partials); lse [T][H] float or NULL.  1 <= H <= 1024, q_group * H < 2^31 / 1024.
  *   The work is cut evenly over the GPU by rows read, so ragged lengths need no split count; partial
- *   results live in ws: lsa_latent_attn_workspace_size bytes, 256-byte aligned, not shared by calls that may
- *   overlap. */
+ *   results live in ws: lsa_latent_attn_workspace_size bytes (42 MB whatever the sizes), 256-byte aligned, not
+ *   shared by calls that may overlap. */
 lsa_status lsa_latent_attn(const lsa_batch* batch, const void* q, int H, const lsa_cache* kv,
                            const lsa_pages* pages, float sm_scale, void* o, int out_dtype, float* lse,
                            void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);

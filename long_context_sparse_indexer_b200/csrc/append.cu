@@ -2,8 +2,9 @@
 //
 // h = norm(x[0:n]) (RMS or layer norm), then the rotation of the rotary part, then BF16 or e4m3 codes with
 // scale = max|row| / 448.  Every element is read once and written once with a few operations in between:
-// bound by memory for many rows (and close behind by instructions) and by the latency of one row for few (32,764 latent
-// rows to BF16 pages 23 us, 3.3 TB/s; as many 128-element keys to FP8 17 us; a decode step's 32 rows 4.4 us).  LANES lanes
+// bound for many rows by the latency of the chain load, reductions, exchange, store with one row ahead (instructions fill
+// about 40% of the issue slots), for few by that of one row (on the device, inputs not in L2: 32,764 latent rows to BF16
+// pages 29 us, 2.6 TB/s, to FP8 39; as many 128-element keys to FP8 17.5; a decode step's 32 rows 4.2).  LANES lanes
 // (32, 16 or 8, the fewest that hold a row in up to four 16-byte chunks each) take a row and keep it in registers, so
 // that its loads travel together and the reductions are shuffles.  A warp takes several rows one after another: the
 // loads that find their places depend on one another (position and sequence, then length and page), so lanes find

@@ -30,11 +30,14 @@
 // BF16: 10 and 11 load keys and exchanged rows by TMA.  FP8: 16 loads a tile's codes into the tail of the stage that they
 // widen into (bit moves only), eight warps widen them there and four the exchanged rows, one brings the row scales, and
 // the plan is 21's.
-// All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.
+// All waits are bounded; a CTA that gives up reports LSA_ERR_TIMEOUT.  A parity tells one phase from the next only, so
+// every wait is on a barrier each phase of which its warp sees, and none of whose phases ends without that warp's part in
+// the one before.
 //
-// Measured: 32 tokens of 128 heads at 32K-64K rows 400 us (1.1 PFLOP/s, 4.6 TB/s; a tile of 64 keys takes 1,470 cycles, 1,244
-// of them products, at 1.4-1.6 GHz under the power limit), FP8 450 us (2,400 cycles: widening); a 500-token chunk behind 15.5K
-// rows 1.3 ms, 1.26 PFLOP/s; one token at 1000 rows 15.9 us, all latency.
+// Measured (kernel and join on the device, inputs not in L2; in brackets after a tenth of a second of such calls, when the GPU
+// is at its power limit, 1.1-1.6 GHz): 32 tokens of 128 heads at 32K-64K rows 396-416 us [470] (1.1 PFLOP/s, 4.6 TB/s; a tile
+// of 64 keys takes 1,470 cycles, 1,244 of them products), FP8 455-463 [530] (2,400 cycles: widening); a chunk of 500 tokens
+// behind 15,500 rows 1.50 ms [1.72], 1.46 [1.27] PFLOP/s; one token at 1000 rows 17.3 us, all latency.
 #include <cmath>
 #include <cstring>
 #include <mutex>

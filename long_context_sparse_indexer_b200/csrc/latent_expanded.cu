@@ -26,8 +26,9 @@
 // reports LSA_ERR_TIMEOUT.  The waits of warps 9 and 11 take the limit of lsa_set_wait_limit_ns, and every other wait
 // ends with the flag that they set; what is in flight then is waited for with the 2 s bound, each with a flag of its own.
 //
-// Measured: 2048 queries behind 2048 keys, 128 heads, causal: 430 us, 1.2 PFLOP/s under the power limit.  A pair of query tiles
-// takes about 3,700 cycles a key tile where its products take 2,560: the chain score, softmax, product shows.
+// Measured on the device: 2048 queries behind 2048 keys, 128 heads, causal: 419-430 us, 1.2 PFLOP/s; 490 us after a tenth of a
+// second of such calls, at the power limit (1.5 GHz).  A pair of query tiles takes about 3,700 cycles a key tile where its
+// products take 2,560: the chain score, softmax, product shows.
 #include <cmath>
 #include <cstring>
 
