@@ -340,8 +340,9 @@ lsa_status lsa_cache_append(const lsa_batch* batch, const void* x, int64_t ld_x,
  * with q_pos[t] < 0 is padding: o = 0, lse = -inf.  A position or a sequence outside the batch is reported
  * and its token treated as padding.  Cached values at rows 0 .. the group's largest q_pos must be finite;
  * what lies behind them may be anything.  A row that lsa_cache_append reported as bad makes the results of
- * the tokens that see it NaN (with a BF16 cache also those of other tokens of their group).  A query with a
- * NaN or an infinity gives NaN (o and lse).  With an FP8 cache 2^-30 <= sm_scale <= 2^30 (others are refused),
+ * the tokens that see it NaN (with a BF16 cache also those of other tokens of their group, while a row with
+ * nothing but infinities among its last 64 elements is left out where its score is -inf).  A query with a NaN or
+ * an infinity gives NaN (o and lse).  With an FP8 cache 2^-30 <= sm_scale <= 2^30 (others are refused),
  * |q| < 2^67 and scale * sm_scale < 2^58; results that stay below 2^-40 / sm_scale lose accuracy.
  *   q [T][H][576] BF16; o [T][H][512] of out_dtype (LSA_BF16, or LSA_FP32 for results that are merged later
  *   with lsa_merge_partials); lse [T][H] float or NULL.  1 <= H <= 1024, q_group * H < 2^31 / 1024.
